@@ -92,7 +92,7 @@ def draw(rng):
     group = rng.choice([1, 2, 3, 4, 7, 8, 16])
     cache = "int8" if dtype != "float32" and rng.random() < 0.25 else dtype
     sink, recent, q_len = rng.choice([0, 1, 2]), rng.choice([1, 2, 3]), rng.choice([1, 1, 1, 2, 3])
-    keep = min(_log(rng, 4, 256), 4096 * 2048 // (size * batch * q_len)) + sink + recent
+    keep = min(_log(rng, 4, 256), 3584 * 2048 // (size * batch * q_len)) + sink + recent
     return _attn(op, batch, lo, hi, q_len, kv * group, kv, d, dtype, cache, keep, sink, recent)
 
 
