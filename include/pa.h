@@ -78,8 +78,14 @@ enum pa_error_flag {
     PA_EFLAG_BAD_SLOT = 2,    /* a slot_mapping entry was >= num_blocks * PA_BLOCK_SIZE */
     PA_EFLAG_BAD_PAIR = 4,    /* a pa_block_copy pair was outside the pool */
     PA_EFLAG_WAIT_TIMEOUT = 8, /* a bounded wait on an asynchronous copy gave up */
-    PA_EFLAG_APPEND_SLOT = 16  /* pa_decode_append: a new token's slot was not the slot of
+    PA_EFLAG_APPEND_SLOT = 16, /* pa_decode_append: a new token's slot was not the slot of
                                   its sequence's position seq_lens[b] - 1 */
+    PA_EFLAG_OUT_OF_BLOCKS = 32, /* pa_step_tables: a sequence was not served, the free list ran out */
+    PA_EFLAG_BAD_LENGTH = 64,    /* a sequence was not served or not covered: a length outside its
+                                    range, more tokens than the slot buffer holds, or tokens for a
+                                    partly filled block that other sequences share */
+    PA_EFLAG_FREE_LIST = 128     /* pa_step_tables: a free count outside [0, num_blocks], more blocks
+                                    given back than the list holds, or a reference count below zero */
 };
 
 #define PA_BLOCK_SIZE 16
@@ -408,6 +414,61 @@ int pa_append_int8(const void *k, const void *v, int src_dtype, int8_t *key_cach
 int pa_quantize_int4(const void *src_cache, int src_dtype, uint8_t *dst_cache, float *scales,
                      int64_t num_blocks, int num_kv_heads, int head_dim, int block_size,
                      pa_stream_t stream);
+
+/*
+ * One step's block tables, slot map, positions and lengths, from the lengths of its
+ * sequences: what the host does between two steps of a decode loop (blocks are handed
+ * out on demand and come back when a sequence ends, lqnn.cn/news/235768 sections 3.2 to
+ * 3.3 and chanyi.net.cn/article/49 section 三), on the device, so that a loop needs no
+ * host between its steps and can be captured into a CUDA graph.
+ *
+ * Sequence b has seq_lens[b] tokens in the cache and new_lens[b] to add (0: none), or
+ * new_lens[b] == PA_SEQ_FINISHED: it has ended.  free_blocks[0 .. free_count[0]-1] is a
+ * stack of the pool's unused blocks, its top at the end.  In this order:
+ *  1. The blocks of the finished sequences (the first ceil(seq_lens[b] / 16) entries of
+ *     their table rows) are pushed, sequence by sequence, block by block.  With
+ *     refcounts, each entry takes one off its block's count, and a block is pushed where
+ *     its last entry of this call brings the count to zero.
+ *  2. The other sequences, in order, get the ceil((seq_lens[b] + new_lens[b]) / 16) -
+ *     ceil(seq_lens[b] / 16) blocks they need, popped one by one, while the list lasts: a
+ *     sequence is served when the needs of the sequences up to it fit into the list, or
+ *     when it needs none.  New blocks go to the next entries of its table row (and get
+ *     refcount 1).
+ * Results:
+ *   seq_lens_out[b]    seq_lens[b] + new_lens[b]; 0 for a finished sequence; seq_lens[b]
+ *                      for one that is not served
+ *   free_count_out[0]  the entries left on the list
+ *   row_starts[b]      tokens of the sequences before b (num_seqs + 1 entries, none above
+ *                      max_tokens): sequence b's new tokens are row_starts[b] ..
+ *                      row_starts[b + 1] - 1, served or not
+ *   slot_mapping[t]    the slot of new token t, -1 when its sequence is not served and for
+ *                      every t past the last token (pa_reshape_and_cache skips those)
+ *   positions[t]       its position in its sequence, or -1
+ * free_blocks keeps its entries beyond those that were pushed; table entries beyond a
+ * row's blocks are neither read nor written.  The order of blocks is that of
+ * BlockManager (free_sequence for the finished ones, then the appends).
+ *
+ * A sequence is not served, with its flag in the error word, when the list ran out
+ * (PA_EFLAG_OUT_OF_BLOCKS), when seq_lens[b] < 0, new_lens[b] < PA_SEQ_FINISHED,
+ * seq_lens[b] + new_lens[b] > 16 * max_blocks_per_seq, its tokens end after max_tokens,
+ * or its last, partly filled block has a refcount above one (PA_EFLAG_BAD_LENGTH; copy
+ * that block first, see pa_block_copy), or when that block's table entry is outside the
+ * pool (PA_EFLAG_BAD_BLOCK).  Entries of finished rows outside the pool are not pushed
+ * (PA_EFLAG_BAD_BLOCK).
+ *
+ * seq_lens_out may be seq_lens, and free_count_out free_count; otherwise the buffers do
+ * not overlap.  refcounts [num_blocks], positions [max_tokens] and row_starts may be NULL.
+ * free_blocks has num_blocks entries.  num_seqs <= PA_STEP_MAX_SEQS, num_seqs *
+ * max_blocks_per_seq <= 2^30 and refcounts below 2^30.  A call with num_seqs == 0 only
+ * fills slot_mapping and positions with -1 and carries the count over.
+ */
+#define PA_SEQ_FINISHED (-1)
+#define PA_STEP_MAX_SEQS 8192
+int pa_step_tables(int32_t *block_tables, const int32_t *seq_lens, const int32_t *new_lens, int32_t *seq_lens_out,
+                   int32_t *free_blocks, const int32_t *free_count, int32_t *free_count_out, int32_t *refcounts,
+                   int64_t *slot_mapping, int32_t *positions, int32_t *row_starts, int num_seqs,
+                   int max_blocks_per_seq, int64_t num_blocks, int64_t max_tokens, int block_size,
+                   pa_stream_t stream);
 
 /*
  * Read the calling thread's current device's error word into *flags

@@ -301,6 +301,24 @@ int pa_append_int8(const void *k, const void *v, int src_dtype, int8_t *key_cach
                               (cudaStream_t)stream);
 }
 
+int pa_step_tables(int32_t *block_tables, const int32_t *seq_lens, const int32_t *new_lens, int32_t *seq_lens_out,
+                   int32_t *free_blocks, const int32_t *free_count, int32_t *free_count_out, int32_t *refcounts,
+                   int64_t *slot_mapping, int32_t *positions, int32_t *row_starts, int num_seqs,
+                   int max_blocks_per_seq, int64_t num_blocks, int64_t max_tokens, int block_size,
+                   pa_stream_t stream) {
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || max_tokens < 0) return PA_ERR_SHAPE;
+    if (block_size != PA_BLOCK_SIZE) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > PA_STEP_MAX_SEQS || (int64_t)num_seqs * max_blocks_per_seq > (1LL << 30) ||
+        max_blocks_per_seq > (1 << 26) || num_blocks > 2147483647LL || max_tokens > 2147483646LL)
+        return PA_ERR_UNSUPPORTED;
+    if (!free_blocks || !free_count || !free_count_out || (max_tokens > 0 && !slot_mapping)) return PA_ERR_NULL;
+    if (num_seqs > 0 && (!block_tables || !seq_lens || !new_lens || !seq_lens_out)) return PA_ERR_NULL;
+    StepArgs a{block_tables, seq_lens,  new_lens,   seq_lens_out, free_blocks,        free_count,
+               free_count_out, refcounts, slot_mapping, positions,  row_starts,   num_seqs, max_blocks_per_seq,
+               (int)num_blocks, (int)max_tokens};
+    return launch_step_tables(a, (cudaStream_t)stream);
+}
+
 size_t pa_decode_workspace_size(const pa_decode_params *p) {
     Plan pl;
     if (make_plan(p, &pl) != PA_OK) return 0;
@@ -538,7 +556,8 @@ int pa_get_error_flags(unsigned int *flags, int reset, pa_stream_t stream) {
     if (!flags) return PA_ERR_NULL;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return PA_ERR_CUDA;
     int (*const words[])(unsigned int *, bool) = {error_word_cache_ops, error_word_decode_simt,
-                                                  error_word_decode_tc, error_word_decode_umma};
+                                                  error_word_decode_tc, error_word_decode_umma,
+                                                  error_word_step_tables};
     unsigned int all = 0;
     for (auto w : words) {
         unsigned int f = 0;

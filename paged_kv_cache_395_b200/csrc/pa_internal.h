@@ -90,11 +90,28 @@ constexpr int kTcMaxChunks = 2048;
 constexpr int kTcMinChunk = PA_TC_MIN_CHUNK;
 constexpr int kTcMaxB = 4096;
 
+// Arguments of pa_step_tables after validation.
+struct StepArgs {
+    int32_t *tables;             // [B][M]
+    const int32_t *lens, *news;  // [B]
+    int32_t *lens_out;           // [B], may be lens
+    int32_t *free_blocks;        // [N]
+    const int32_t *count;
+    int32_t *count_out;          // may be count
+    int32_t *refs;               // [N] or NULL
+    int64_t *slots;              // [T]
+    int32_t *pos;                // [T] or NULL
+    int32_t *starts;             // [B + 1] or NULL
+    int B, M, N, T;
+};
+int launch_step_tables(const StepArgs &a, cudaStream_t st);
+
 // Per-translation-unit error words (see PA_ERROR_WORD_ACCESSOR).
 int error_word_cache_ops(unsigned int *flags, bool reset);
 int error_word_decode_simt(unsigned int *flags, bool reset);
 int error_word_decode_tc(unsigned int *flags, bool reset);
 int error_word_decode_umma(unsigned int *flags, bool reset);
+int error_word_step_tables(unsigned int *flags, bool reset);
 
 // Raise a kernel's dynamic shared-memory limit on the current device, once per
 // (kernel, device).  Thread-safe; returns false if CUDA refuses.

@@ -5,7 +5,7 @@ The names mirror the C ABI in ``include/pa.h``:
 * ``pa_reshape_and_cache``, ``pa_decode``, ``pa_decode_append``,
   ``pa_decode_append_fused``, ``pa_decode_fixed_scratch``,
   ``pa_decode_stall_selftest``, ``pa_block_copy``, ``pa_quantize_int8``,
-  ``pa_quantize_int4``, ``pa_append_int8``, ``pa_decode_workspace_size``,
+  ``pa_quantize_int4``, ``pa_append_int8``, ``pa_step_tables``, ``pa_decode_workspace_size``,
   ``pa_decode_algo``, ``pa_get_error_flags`` take torch CUDA tensors (or raw device pointers via ``lib``), check device,
   dtype and contiguity, and call the library on
   ``torch.cuda.current_stream()``.  Every step of the computation runs in the
@@ -30,6 +30,8 @@ PA_F32, PA_F16, PA_BF16, PA_I8, PA_I4 = 0, 1, 2, 3, 4
 PA_ALGO_AUTO, PA_ALGO_SIMT, PA_ALGO_TENSOR, PA_ALGO_TCGEN05 = 0, 1, 2, 3
 PA_EFLAG_BAD_BLOCK, PA_EFLAG_BAD_SLOT, PA_EFLAG_BAD_PAIR, PA_EFLAG_WAIT_TIMEOUT = 1, 2, 4, 8
 PA_EFLAG_APPEND_SLOT = 16
+PA_EFLAG_OUT_OF_BLOCKS, PA_EFLAG_BAD_LENGTH, PA_EFLAG_FREE_LIST = 32, 64, 128
+PA_SEQ_FINISHED, PA_STEP_MAX_SEQS = -1, 8192
 PA_DECODE_INPUTS_READY, PA_DECODE_OUT_F32 = 1, 2
 PA_APPEND_OVERLAP_PREVIOUS = 1
 BLOCK_SIZE = 16
@@ -86,6 +88,7 @@ def _load():
     L.pa_quantize_int8.argtypes = [P, i32, P, P, i64, i32, i32, i32, P]
     L.pa_append_int8.argtypes = [P, P, i32, P, P, P, P, P, i64, i32, i32, i32, i64, i64, i64, P]
     L.pa_quantize_int4.argtypes = [P, i32, P, P, i64, i32, i32, i32, P]
+    L.pa_step_tables.argtypes = [P] * 11 + [i32, i32, i64, i64, i32, P]
     L.pa_get_error_flags.argtypes = [ctypes.POINTER(ctypes.c_uint), i32, P]
     L.pa_status_string.argtypes = [i32]
     L.pa_status_string.restype = ctypes.c_char_p
@@ -93,7 +96,7 @@ def _load():
     for n in ("pa_reshape_and_cache", "pa_reshape_and_cache_ex", "pa_append_int8", "pa_decode", "pa_decode_append",
               "pa_decode_append_fused", "pa_decode_fixed_scratch",
               "pa_decode_stall_selftest", "pa_decode_algo", "pa_decode_launches", "pa_block_copy",
-              "pa_quantize_int8", "pa_quantize_int4", "pa_get_error_flags", "pa_version"):
+              "pa_quantize_int8", "pa_quantize_int4", "pa_step_tables", "pa_get_error_flags", "pa_version"):
         getattr(L, n).restype = i32
     return L
 
@@ -104,7 +107,7 @@ lib = _load()
 EXPORTED = ("pa_reshape_and_cache", "pa_reshape_and_cache_ex", "pa_append_int8", "pa_decode_workspace_size",
             "pa_decode_algo", "pa_decode_launches", "pa_decode", "pa_decode_append", "pa_decode_append_fused",
             "pa_decode_fixed_scratch", "pa_decode_stall_selftest", "pa_block_copy", "pa_quantize_int8",
-            "pa_quantize_int4", "pa_get_error_flags", "pa_status_string", "pa_version")
+            "pa_quantize_int4", "pa_step_tables", "pa_get_error_flags", "pa_status_string", "pa_version")
 FIXED_SCRATCH_BYTES = 32 << 20  # PA_FIXED_SCRATCH_BYTES
 
 
@@ -400,6 +403,57 @@ def pa_quantize_int4(src_cache, dst_cache, scales, stream=None):
         raise ValueError("scales must be float32")
     _check(lib.pa_quantize_int4(_ptr(src_cache), dtype_code(src_cache.dtype), _ptr(dst_cache),
                                 _ptr(scales), N, H, d, bs, _stream(stream)), "pa_quantize_int4")
+
+
+def _here(*ts) -> int:
+    """The current device, where every tensor has to be: a call launches on its stream."""
+    devs = {t.get_device() for t in ts if t is not None}
+    if -1 in devs:
+        raise ValueError("all tensors must be CUDA tensors")
+    dev = torch.cuda.current_device()
+    if devs != {dev}:
+        raise ValueError("all tensors must be on the current device")
+    return dev
+
+
+def _stream_on(dev: int, stream):
+    """The raw handle of the stream, by default the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def pa_step_tables(block_tables, seq_lens, new_lens, free_blocks, free_count, slot_mapping, seq_lens_out=None,
+                   free_count_out=None, positions=None, row_starts=None, refcounts=None, stream=None):
+    """One step's block tables, slots, positions and lengths from the sequences'
+    lengths (see include/pa.h).  block_tables int32 [B][M] (updated in place);
+    seq_lens, new_lens int32 [B] (new_lens PA_SEQ_FINISHED: the sequence ended);
+    free_blocks int32 [N], a stack of the pool's N blocks of which the first
+    free_count (int32 [1]) are unused (updated in place); slot_mapping int64 [T],
+    filled, with -1 past the step's tokens; positions int32 [T]; row_starts int32
+    [B + 1]; refcounts int32 [N] (updated in place).  Without seq_lens_out /
+    free_count_out the inputs are updated in place."""
+    lens_out = seq_lens if seq_lens_out is None else seq_lens_out
+    count_out = free_count if free_count_out is None else free_count_out
+    dev = _here(block_tables, seq_lens, new_lens, lens_out, free_blocks, free_count, count_out, slot_mapping, positions,
+                row_starts, refcounts)
+    i32 = torch.int32
+    B, M = block_tables.shape
+    N, T = free_blocks.numel(), slot_mapping.numel()
+    for t, n, name in ((block_tables, B * M, "block_tables"), (seq_lens, B, "seq_lens"), (new_lens, B, "new_lens"),
+                       (lens_out, B, "seq_lens_out"), (free_blocks, N, "free_blocks"), (free_count, 1, "free_count"),
+                       (count_out, 1, "free_count_out"), (positions, T, "positions"), (row_starts, B + 1, "row_starts"),
+                       (refcounts, N, "refcounts")):
+        if t is not None and (t.dtype != i32 or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous int32 with {n} elements")
+    if slot_mapping.dtype != torch.int64 or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be contiguous int64")
+    _check(lib.pa_step_tables(_addr(block_tables), _addr(seq_lens), _addr(new_lens), _addr(lens_out), _addr(free_blocks),
+                              _addr(free_count), _addr(count_out), _addr(refcounts), _addr(slot_mapping),
+                              _addr(positions), _addr(row_starts), B, M, N, T, BLOCK_SIZE, _stream_on(dev, stream)),
+           "pa_step_tables")
 
 
 def pa_get_error_flags(reset: bool = True, stream=None) -> int:
