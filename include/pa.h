@@ -471,6 +471,87 @@ int pa_step_tables(int32_t *block_tables, const int32_t *seq_lens, const int32_t
                    pa_stream_t stream);
 
 /*
+ * Block-sparse decode: attention over the blocks that a cheap score picks for each query
+ * row and KV head, for contexts so long that reading the whole cache bounds the step.
+ * (No counterpart in the pages.)  Next to the cache, each (block, KV head) keeps the box
+ * of its 16 keys in eight bits a side, 1/32 of the fp16 K and V bytes:
+ *   bounds        [num_blocks][num_kv_heads][2][head_dim]  int8: lower, then upper codes
+ *   bound_scales  [num_blocks][num_kv_heads]  fp32
+ * pa_block_bounds fills it for the blocks that became full, pa_select_blocks scores and
+ * picks, pa_decode_selected attends, and pa_decode_sparse does both in one call.
+ *
+ * A query row is one (sequence, new token) pair: row (b, t) sees the first L =
+ * seq_lens[b] - Q + 1 + t tokens of sequence b, as in pa_decode with query_len Q, and
+ * n = ceil(L / 16) blocks.
+ */
+
+/*
+ * Boxes of the blocks that sequence b filled: blocks floor(first_lens[b] / 16) ..
+ * floor(seq_lens[b] / 16) - 1 of its table row (first_lens NULL: from block 0), each KV
+ * head.  In IEEE fp32, over the 16 keys of the tile, per dim j:
+ *   lo_j = min, hi_j = max,  a = max_j max(|lo_j|, |hi_j|),  s = a / 127
+ *   bounds = clamp(floor(lo_j / s)), clamp(ceil(hi_j / s)) to [-127, 127];  scale = s
+ * s == 0 gives codes 0; a tile that holds an infinity or a NaN gets scale +inf and codes
+ * 0 (pa_select_blocks then prefers it, so that what dense attention would show is seen).
+ * An int8 cache's keys are q8 * k_scale.  A block in several tables is written the same
+ * by each.  The box of a partly filled block is not needed: a row's newest block is always
+ * picked.
+ * Covered are at most ceil(max_new_tokens / 16) blocks per sequence; a sequence that grew
+ * by more sets PA_EFLAG_BAD_LENGTH.  Lengths above 16 * max_blocks_per_seq are cut to it.
+ * Table entries outside the pool set PA_EFLAG_BAD_BLOCK and are skipped.
+ * kv_dtype: PA_F32, PA_F16, PA_BF16 or PA_I8 (then k_scales); head_dim 64, 128 or 256.
+ * key_cache and bounds are 16-byte aligned.
+ */
+int pa_block_bounds(int8_t *bounds, float *bound_scales, const void *key_cache, const float *k_scales,
+                    const int32_t *block_tables, const int32_t *first_lens, const int32_t *seq_lens, int num_seqs,
+                    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                    int64_t max_new_tokens, int kv_dtype, pa_stream_t stream);
+
+typedef struct pa_sparse_params {
+    int num_seqs;           /* B >= 0 */
+    int num_q_heads;        /* a multiple of num_kv_heads, up to 64 query heads per KV head */
+    int num_kv_heads;
+    int head_dim;           /* 64, 128 or 256 */
+    int block_size;         /* must be PA_BLOCK_SIZE */
+    int max_blocks_per_seq; /* row stride of block_tables */
+    int64_t num_blocks;
+    int max_seq_len;        /* >= every seq_lens[b], up to PA_SPARSE_MAX_SEQ_LEN; tokens beyond it or
+                               beyond max_blocks_per_seq * 16 are ignored */
+    int q_dtype;            /* PA_F32, PA_F16 or PA_BF16 */
+    int kv_dtype;           /* q_dtype, or PA_I8 with a PA_F16 or PA_BF16 q */
+    const float *k_scales;  /* PA_I8 only: [num_blocks][num_kv_heads], else NULL */
+    const float *v_scales;
+    int query_len;          /* new tokens per sequence, Q (0 or 1: single-token decode): q and out are
+                               [num_seqs][Q][num_q_heads][head_dim] */
+    int max_selected;       /* K: entries per row and KV head of `selected` */
+    int sink_blocks;        /* the row's first blocks, always picked */
+    int recent_blocks;      /* and its last ones, >= 1; sink_blocks + recent_blocks <= K */
+    int flags;              /* 0 or PA_DECODE_OUT_F32 */
+} pa_sparse_params;
+#define PA_SPARSE_MAX_SEQ_LEN 524288
+
+/*
+ * The blocks each query row and KV head attends to:
+ *   selected      [num_seqs * Q][num_kv_heads][K]  int32: logical blocks, ascending, then -1
+ *   num_selected  [num_seqs * Q][num_kv_heads]     int32: min(n, K)
+ * A row with n <= K takes all its blocks.  Otherwise the first sink_blocks, the last
+ * recent_blocks and, of the others, those with the highest score, the lower index first
+ * among equals.  The score estimates from above the largest product of a query head with
+ * a key of the block; with q's codes of head g, in IEEE fp32,
+ *   s_g = max_j |q_j| / 127,  c_j = clamp(round_half_even(q_j / s_g), -127, 127)
+ *   score = max_g (sum_j max(c_j * lo_j, c_j * hi_j)) * scale * s_g
+ * over the query heads g of the KV head; the sum is of whole numbers, so the result does
+ * not depend on any order of summation.  A head whose s_g is 0 or not finite has codes 0
+ * and s_g = 0.  A block whose scale is not finite scores +inf; one outside the pool scores
+ * lowest (PA_EFLAG_BAD_BLOCK).  The boxes of the last recent_blocks are not used.
+ * bounds 16-byte aligned.  Reads the fields of p that it names; k_scales, v_scales and
+ * flags are not used.
+ */
+int pa_select_blocks(int32_t *selected, int32_t *num_selected, const void *q, const int8_t *bounds,
+                     const float *bound_scales, const int32_t *block_tables, const int32_t *seq_lens,
+                     const pa_sparse_params *p, pa_stream_t stream);
+
+/*
  * Read the calling thread's current device's error word into *flags
  * (pa_error_flag bits); synchronises `stream` first.  reset != 0 clears it.
  */

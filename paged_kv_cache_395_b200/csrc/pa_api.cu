@@ -319,6 +319,28 @@ int pa_step_tables(int32_t *block_tables, const int32_t *seq_lens, const int32_t
     return launch_step_tables(a, (cudaStream_t)stream);
 }
 
+int pa_block_bounds(int8_t *bounds, float *bound_scales, const void *key_cache, const float *k_scales,
+                    const int32_t *block_tables, const int32_t *first_lens, const int32_t *seq_lens, int num_seqs,
+                    int num_kv_heads, int head_dim, int block_size, int max_blocks_per_seq, int64_t num_blocks,
+                    int64_t max_new_tokens, int kv_dtype, pa_stream_t stream) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || head_dim <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 ||
+        max_new_tokens < 0)
+        return PA_ERR_SHAPE;
+    if (kv_dtype != PA_F32 && kv_dtype != PA_F16 && kv_dtype != PA_BF16 && kv_dtype != PA_I8) return PA_ERR_DTYPE;
+    if (block_size != PA_BLOCK_SIZE || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        num_kv_heads > 65535 || max_blocks_per_seq > (1 << 26))
+        return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0 || max_new_tokens == 0) return PA_OK;
+    if (!bounds || !bound_scales || !key_cache || !block_tables || !seq_lens || (kv_dtype == PA_I8 && !k_scales))
+        return PA_ERR_NULL;
+    if (((uintptr_t)key_cache | (uintptr_t)bounds) % 16) return PA_ERR_ALIGN;
+    const int64_t w = (max_new_tokens + PA_BLOCK_SIZE - 1) / PA_BLOCK_SIZE;
+    const BoundsArgs a{bounds, bound_scales, key_cache, k_scales, block_tables, first_lens, seq_lens, num_seqs,
+                       num_kv_heads, head_dim, max_blocks_per_seq,
+                       (int)(w < max_blocks_per_seq ? w : max_blocks_per_seq), num_blocks, kv_dtype};
+    return launch_block_bounds(a, (cudaStream_t)stream);
+}
+
 size_t pa_decode_workspace_size(const pa_decode_params *p) {
     Plan pl;
     if (make_plan(p, &pl) != PA_OK) return 0;
@@ -552,12 +574,77 @@ int pa_decode_launches(const pa_decode_params *p, const void *q) {
     return pl.bytes > 0 ? 2 : 1;  // merge_tc_kernel after a split decode
 }
 
+}  // extern "C"
+
+namespace pa {
+
+// The checks that the block-sparse calls share; fills the kernels' view of p.
+static int sparse_args(const pa_sparse_params *p, SparseArgs *a) {
+    if (!p) return PA_ERR_NULL;
+    const int Q = p->query_len > 1 ? p->query_len : 1;
+    if (p->num_seqs < 0 || p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->head_dim <= 0 ||
+        p->max_blocks_per_seq <= 0 || p->num_blocks <= 0 || p->max_seq_len < 0 || p->query_len < 0 ||
+        p->num_q_heads % p->num_kv_heads)
+        return PA_ERR_SHAPE;
+    if (p->max_selected <= 0 || p->sink_blocks < 0 || p->recent_blocks < 1 ||
+        (int64_t)p->sink_blocks + p->recent_blocks > p->max_selected)
+        return PA_ERR_SHAPE;
+    if (p->q_dtype != PA_F32 && p->q_dtype != PA_F16 && p->q_dtype != PA_BF16) return PA_ERR_DTYPE;
+    if (p->kv_dtype != p->q_dtype && (p->kv_dtype != PA_I8 || p->q_dtype == PA_F32)) return PA_ERR_DTYPE;
+    if (p->block_size != PA_BLOCK_SIZE || (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) ||
+        p->num_q_heads / p->num_kv_heads > 64 || p->max_blocks_per_seq > (1 << 26) ||
+        p->max_selected > PA_SPARSE_MAX_SEQ_LEN / PA_BLOCK_SIZE || p->num_kv_heads > 65535 ||
+        (int64_t)p->num_seqs * Q * p->num_kv_heads > (1 << 26) || (p->flags & ~PA_DECODE_OUT_F32))
+        return PA_ERR_UNSUPPORTED;
+    const int cap = p->max_blocks_per_seq * PA_BLOCK_SIZE;
+    *a = SparseArgs{};
+    a->max_len = p->max_seq_len < cap ? p->max_seq_len : cap;
+    if (a->max_len > PA_SPARSE_MAX_SEQ_LEN) return PA_ERR_UNSUPPORTED;
+    a->rows = p->num_seqs * Q;
+    a->Q = Q;
+    a->Hq = p->num_q_heads;
+    a->H = p->num_kv_heads;
+    a->G = p->num_q_heads / p->num_kv_heads;
+    a->D = p->head_dim;
+    a->M = p->max_blocks_per_seq;
+    a->K = p->max_selected;
+    a->sink = p->sink_blocks;
+    a->recent = p->recent_blocks;
+    a->N = p->num_blocks;
+    a->q_dtype = p->q_dtype;
+    a->kv_dtype = p->kv_dtype;
+    return PA_OK;
+}
+
+}  // namespace pa
+
+extern "C" {
+
+int pa_select_blocks(int32_t *selected, int32_t *num_selected, const void *q, const int8_t *bounds,
+                     const float *bound_scales, const int32_t *block_tables, const int32_t *seq_lens,
+                     const pa_sparse_params *p, pa_stream_t stream) {
+    SparseArgs a;
+    const int rc = sparse_args(p, &a);
+    if (rc != PA_OK) return rc;
+    if (a.rows == 0) return PA_OK;
+    if (!selected || !num_selected || !q || !bounds || !bound_scales || !block_tables || !seq_lens) return PA_ERR_NULL;
+    if ((uintptr_t)bounds % 16) return PA_ERR_ALIGN;
+    a.sel = selected;
+    a.nsel = num_selected;
+    a.q = q;
+    a.bounds = bounds;
+    a.bscales = bound_scales;
+    a.tables = block_tables;
+    a.lens = seq_lens;
+    return launch_select_blocks(a, (cudaStream_t)stream);
+}
+
 int pa_get_error_flags(unsigned int *flags, int reset, pa_stream_t stream) {
     if (!flags) return PA_ERR_NULL;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return PA_ERR_CUDA;
     int (*const words[])(unsigned int *, bool) = {error_word_cache_ops, error_word_decode_simt,
                                                   error_word_decode_tc, error_word_decode_umma,
-                                                  error_word_step_tables};
+                                                  error_word_step_tables, error_word_sparse_select};
     unsigned int all = 0;
     for (auto w : words) {
         unsigned int f = 0;

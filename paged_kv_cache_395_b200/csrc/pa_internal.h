@@ -106,12 +106,39 @@ struct StepArgs {
 };
 int launch_step_tables(const StepArgs &a, cudaStream_t st);
 
+// Arguments of the block-sparse operators after validation.
+struct BoundsArgs {
+    int8_t *bounds;
+    float *scales;
+    const void *kc;
+    const float *ks;
+    const int32_t *tables, *first, *lens;
+    int B, H, D, M, W;  // W: blocks per sequence at most
+    int64_t N;
+    int kv_dtype;
+};
+int launch_block_bounds(const BoundsArgs &a, cudaStream_t st);
+
+struct SparseArgs {
+    int32_t *sel, *nsel;  // [rows][H][K], [rows][H]
+    const void *q;
+    const int8_t *bounds;
+    const float *bscales;
+    const int32_t *tables, *lens;
+    int rows, Q, Hq, H, G, D, M, K, sink, recent;  // rows = B * Q
+    int64_t N;
+    int max_len;  // effective bound on lengths
+    int q_dtype, kv_dtype;
+};
+int launch_select_blocks(const SparseArgs &a, cudaStream_t st);
+
 // Per-translation-unit error words (see PA_ERROR_WORD_ACCESSOR).
 int error_word_cache_ops(unsigned int *flags, bool reset);
 int error_word_decode_simt(unsigned int *flags, bool reset);
 int error_word_decode_tc(unsigned int *flags, bool reset);
 int error_word_decode_umma(unsigned int *flags, bool reset);
 int error_word_step_tables(unsigned int *flags, bool reset);
+int error_word_sparse_select(unsigned int *flags, bool reset);
 
 // Raise a kernel's dynamic shared-memory limit on the current device, once per
 // (kernel, device).  Thread-safe; returns false if CUDA refuses.

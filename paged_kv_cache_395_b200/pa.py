@@ -5,7 +5,8 @@ The names mirror the C ABI in ``include/pa.h``:
 * ``pa_reshape_and_cache``, ``pa_decode``, ``pa_decode_append``,
   ``pa_decode_append_fused``, ``pa_decode_fixed_scratch``,
   ``pa_decode_stall_selftest``, ``pa_block_copy``, ``pa_quantize_int8``,
-  ``pa_quantize_int4``, ``pa_append_int8``, ``pa_step_tables``, ``pa_decode_workspace_size``,
+  ``pa_quantize_int4``, ``pa_append_int8``, ``pa_step_tables``,
+  ``pa_block_bounds``, ``pa_select_blocks``, ``pa_decode_workspace_size``,
   ``pa_decode_algo``, ``pa_get_error_flags`` take torch CUDA tensors (or raw device pointers via ``lib``), check device,
   dtype and contiguity, and call the library on
   ``torch.cuda.current_stream()``.  Every step of the computation runs in the
@@ -31,7 +32,7 @@ PA_ALGO_AUTO, PA_ALGO_SIMT, PA_ALGO_TENSOR, PA_ALGO_TCGEN05 = 0, 1, 2, 3
 PA_EFLAG_BAD_BLOCK, PA_EFLAG_BAD_SLOT, PA_EFLAG_BAD_PAIR, PA_EFLAG_WAIT_TIMEOUT = 1, 2, 4, 8
 PA_EFLAG_APPEND_SLOT = 16
 PA_EFLAG_OUT_OF_BLOCKS, PA_EFLAG_BAD_LENGTH, PA_EFLAG_FREE_LIST = 32, 64, 128
-PA_SEQ_FINISHED, PA_STEP_MAX_SEQS = -1, 8192
+PA_SEQ_FINISHED, PA_STEP_MAX_SEQS, PA_SPARSE_MAX_SEQ_LEN = -1, 8192, 524288
 PA_DECODE_INPUTS_READY, PA_DECODE_OUT_F32 = 1, 2
 PA_APPEND_OVERLAP_PREVIOUS = 1
 BLOCK_SIZE = 16
@@ -69,6 +70,29 @@ class PaDecodeParams(ctypes.Structure):
     ]
 
 
+class PaSparseParams(ctypes.Structure):
+    """Mirror of ``pa_sparse_params``."""
+    _fields_ = [
+        ("num_seqs", ctypes.c_int),
+        ("num_q_heads", ctypes.c_int),
+        ("num_kv_heads", ctypes.c_int),
+        ("head_dim", ctypes.c_int),
+        ("block_size", ctypes.c_int),
+        ("max_blocks_per_seq", ctypes.c_int),
+        ("num_blocks", ctypes.c_int64),
+        ("max_seq_len", ctypes.c_int),
+        ("q_dtype", ctypes.c_int),
+        ("kv_dtype", ctypes.c_int),
+        ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p),
+        ("query_len", ctypes.c_int),
+        ("max_selected", ctypes.c_int),
+        ("sink_blocks", ctypes.c_int),
+        ("recent_blocks", ctypes.c_int),
+        ("flags", ctypes.c_int),
+    ]
+
+
 def _load():
     L = ctypes.CDLL(LIB_PATH)
     P, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
@@ -89,6 +113,8 @@ def _load():
     L.pa_append_int8.argtypes = [P, P, i32, P, P, P, P, P, i64, i32, i32, i32, i64, i64, i64, P]
     L.pa_quantize_int4.argtypes = [P, i32, P, P, i64, i32, i32, i32, P]
     L.pa_step_tables.argtypes = [P] * 11 + [i32, i32, i64, i64, i32, P]
+    L.pa_block_bounds.argtypes = [P] * 7 + [i32] * 5 + [i64, i64, i32, P]
+    L.pa_select_blocks.argtypes = [P] * 7 + [ctypes.POINTER(PaSparseParams), P]
     L.pa_get_error_flags.argtypes = [ctypes.POINTER(ctypes.c_uint), i32, P]
     L.pa_status_string.argtypes = [i32]
     L.pa_status_string.restype = ctypes.c_char_p
@@ -96,7 +122,8 @@ def _load():
     for n in ("pa_reshape_and_cache", "pa_reshape_and_cache_ex", "pa_append_int8", "pa_decode", "pa_decode_append",
               "pa_decode_append_fused", "pa_decode_fixed_scratch",
               "pa_decode_stall_selftest", "pa_decode_algo", "pa_decode_launches", "pa_block_copy",
-              "pa_quantize_int8", "pa_quantize_int4", "pa_step_tables", "pa_get_error_flags", "pa_version"):
+              "pa_quantize_int8", "pa_quantize_int4", "pa_step_tables", "pa_block_bounds", "pa_select_blocks",
+              "pa_get_error_flags", "pa_version"):
         getattr(L, n).restype = i32
     return L
 
@@ -107,7 +134,8 @@ lib = _load()
 EXPORTED = ("pa_reshape_and_cache", "pa_reshape_and_cache_ex", "pa_append_int8", "pa_decode_workspace_size",
             "pa_decode_algo", "pa_decode_launches", "pa_decode", "pa_decode_append", "pa_decode_append_fused",
             "pa_decode_fixed_scratch", "pa_decode_stall_selftest", "pa_block_copy", "pa_quantize_int8",
-            "pa_quantize_int4", "pa_step_tables", "pa_get_error_flags", "pa_status_string", "pa_version")
+            "pa_quantize_int4", "pa_step_tables", "pa_block_bounds", "pa_select_blocks", "pa_get_error_flags",
+            "pa_status_string", "pa_version")
 FIXED_SCRATCH_BYTES = 32 << 20  # PA_FIXED_SCRATCH_BYTES
 
 
@@ -454,6 +482,82 @@ def pa_step_tables(block_tables, seq_lens, new_lens, free_blocks, free_count, sl
                               _addr(free_count), _addr(count_out), _addr(refcounts), _addr(slot_mapping),
                               _addr(positions), _addr(row_starts), B, M, N, T, BLOCK_SIZE, _stream_on(dev, stream)),
            "pa_step_tables")
+
+
+def _contiguous(**ts):
+    for name, t in ts.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _boxes(bounds, bound_scales, N, H, d):
+    """bounds int8 [N][H_kv][2][d] and their scales fp32 [N][H_kv]."""
+    if bounds.dtype != torch.int8 or tuple(bounds.shape) != (N, H, 2, d) or not bounds.is_contiguous():
+        raise ValueError("bounds must be contiguous int8 [N][H_kv][2][d]")
+    if bound_scales.dtype != torch.float32 or tuple(bound_scales.shape) != (N, H) or not bound_scales.is_contiguous():
+        raise ValueError("bound_scales must be contiguous float32 [N][H_kv]")
+
+
+def pa_block_bounds(bounds, bound_scales, key_cache, block_tables, seq_lens, max_new_tokens, first_lens=None,
+                    k_scales=None, stream=None):
+    """Boxes of the blocks that filled up: for each sequence the full blocks between
+    first_lens (int32 [B], tokens whose blocks have their boxes; None: 0) and seq_lens,
+    at most ceil(max_new_tokens / 16) of them (see include/pa.h).  bounds int8
+    [N][H_kv][2][d], bound_scales fp32 [N][H_kv] (updated in place); key_cache
+    [N][H_kv][16][d] fp32/fp16/bf16, or int8 with k_scales [N][H_kv]."""
+    dev = _here(bounds, bound_scales, key_cache, block_tables, seq_lens, first_lens, k_scales)
+    N, H, bs, d = key_cache.shape
+    B, M = block_tables.shape
+    _boxes(bounds, bound_scales, N, H, d)
+    _contiguous(key_cache=key_cache, block_tables=block_tables, k_scales=k_scales)
+    i32 = torch.int32
+    if block_tables.dtype != i32:
+        raise ValueError("block_tables must be int32")
+    for t, name in ((seq_lens, "seq_lens"), (first_lens, "first_lens")):
+        if t is not None and (t.dtype != i32 or t.numel() != B or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous int32 with {B} elements")
+    if k_scales is not None and (k_scales.dtype != torch.float32 or tuple(k_scales.shape) != (N, H)):
+        raise ValueError("k_scales must be float32 [N][H_kv]")
+    _check(lib.pa_block_bounds(_addr(bounds), _addr(bound_scales), _addr(key_cache), _addr(k_scales),
+                               _addr(block_tables), _addr(first_lens), _addr(seq_lens), B, H, d, bs, M, N,
+                               int(max_new_tokens), dtype_code(key_cache.dtype), _stream_on(dev, stream)),
+           "pa_block_bounds")
+
+
+def _sparse_params(q, H, N, block_tables, seq_lens, selected, num_selected, max_seq_len, sink_blocks, recent_blocks,
+                   kv_dtype, k_scales=None, v_scales=None, flags=0):
+    """Checks what the block-sparse calls share; q [B][H_q][d] or [B][Q][H_q][d]."""
+    shape = q.shape
+    Q = shape[1] if len(shape) == 4 else 1
+    B, Hq, d = shape[0], shape[-2], shape[-1]
+    lead = shape[:-2]
+    K = selected.shape[-1]
+    i32 = torch.int32
+    if len(shape) not in (3, 4) or selected.shape[:-1] != lead + (H,) or num_selected.shape != lead + (H,):
+        raise ValueError("selected must be q's leading sizes, then [H_kv][K], and num_selected the same without K")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B:
+        raise ValueError("block_tables must be [B][M] and seq_lens [B]")
+    if not (selected.dtype == num_selected.dtype == block_tables.dtype == seq_lens.dtype == i32):
+        raise ValueError("selected, num_selected, block_tables and seq_lens must be int32")
+    _contiguous(q=q, selected=selected, num_selected=num_selected, block_tables=block_tables, seq_lens=seq_lens)
+    return PaSparseParams(B, Hq, H, d, BLOCK_SIZE, block_tables.shape[1], N, int(max_seq_len), dtype_code(q.dtype),
+                          kv_dtype, _addr(k_scales), _addr(v_scales), Q, K, int(sink_blocks), int(recent_blocks), flags)
+
+
+def pa_select_blocks(selected, num_selected, q, bounds, bound_scales, block_tables, seq_lens, max_seq_len,
+                     sink_blocks=1, recent_blocks=2, stream=None):
+    """The blocks that each query row and KV head attends to (see include/pa.h):
+    selected int32 [B][H_kv][K] (or [B][Q][H_kv][K]), filled with logical blocks,
+    ascending, then -1; num_selected int32 without the K.  q [B][H_q][d] or
+    [B][Q][H_q][d]; bounds, bound_scales as pa_block_bounds leaves them."""
+    dev = _here(selected, num_selected, q, bounds, bound_scales, block_tables, seq_lens)
+    N, H = bound_scales.shape
+    _boxes(bounds, bound_scales, N, H, q.shape[-1])
+    p = _sparse_params(q, H, N, block_tables, seq_lens, selected, num_selected, max_seq_len, sink_blocks,
+                       recent_blocks, dtype_code(q.dtype))
+    _check(lib.pa_select_blocks(selected.data_ptr(), num_selected.data_ptr(), q.data_ptr(), bounds.data_ptr(),
+                                bound_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
+                                ctypes.byref(p), _stream_on(dev, stream)), "pa_select_blocks")
 
 
 def pa_get_error_flags(reset: bool = True, stream=None) -> int:
