@@ -552,6 +552,30 @@ int pa_select_blocks(int32_t *selected, int32_t *num_selected, const void *q, co
                      const pa_sparse_params *p, pa_stream_t stream);
 
 /*
+ * Decode attention over chosen blocks:
+ *   out[r][g][:] = sum_t softmax_t(scale * q[r][g] . K[t]) V[t]
+ * over the tokens t < L of the blocks selected[r][h][0 .. num_selected[r][h] - 1] of query
+ * row r (KV head h of query head g, L and rows as above).  The lists may be those of
+ * pa_select_blocks for this call's q, or any others (of an earlier layer, say): entries may
+ * stand in any order, each counts as often as it stands there, and those outside [0, n) are
+ * skipped.  Table entries outside the pool are skipped with PA_EFLAG_BAD_BLOCK.  A row with
+ * no token left gives zeros.  Precision, int8 caches and PA_DECODE_OUT_F32 as in pa_decode;
+ * num_blocks * num_kv_heads < 2^31.  One launch, no workspace.
+ * sink_blocks and recent_blocks of p are checked and not used.
+ */
+int pa_decode_selected(void *out, const void *q, const void *key_cache, const void *value_cache,
+                       const int32_t *block_tables, const int32_t *seq_lens, const int32_t *selected,
+                       const int32_t *num_selected, float scale, const pa_sparse_params *p, pa_stream_t stream);
+
+/*
+ * pa_select_blocks, then pa_decode_selected with its lists, in one call.  selected and
+ * num_selected hold the lists afterwards.
+ */
+int pa_decode_sparse(void *out, const void *q, const void *key_cache, const void *value_cache, const int8_t *bounds,
+                     const float *bound_scales, const int32_t *block_tables, const int32_t *seq_lens, int32_t *selected,
+                     int32_t *num_selected, float scale, const pa_sparse_params *p, pa_stream_t stream);
+
+/*
  * Read the calling thread's current device's error word into *flags
  * (pa_error_flag bits); synchronises `stream` first.  reset != 0 clears it.
  */

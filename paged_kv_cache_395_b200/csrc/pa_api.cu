@@ -639,12 +639,75 @@ int pa_select_blocks(int32_t *selected, int32_t *num_selected, const void *q, co
     return launch_select_blocks(a, (cudaStream_t)stream);
 }
 
+}  // extern "C"
+
+namespace pa {
+
+// The attention half's operands, after sparse_args.
+static int attend_args(const pa_sparse_params *p, SparseArgs *a, void *out, const void *q, const void *kc, const void *vc,
+                       const int32_t *tables, const int32_t *lens, int32_t *sel, int32_t *nsel, float scale) {
+    if (!out || !q || !kc || !vc || !tables || !lens || !sel || !nsel) return PA_ERR_NULL;
+    if (p->kv_dtype == PA_I8 && (!p->k_scales || !p->v_scales)) return PA_ERR_NULL;
+    if (((uintptr_t)kc | (uintptr_t)vc) % 16) return PA_ERR_ALIGN;
+    // tiles are numbered with 32-bit integers
+    if (p->num_blocks * (int64_t)p->num_kv_heads > 2147483647LL || p->num_blocks > 2147483647LL) return PA_ERR_UNSUPPORTED;
+    a->out = out;
+    a->q = q;
+    a->kc = kc;
+    a->vc = vc;
+    a->ks = p->k_scales;
+    a->vs = p->v_scales;
+    a->tables = tables;
+    a->lens = lens;
+    a->sel = sel;
+    a->nsel = nsel;
+    a->scale_log2 = scale * kLog2e;
+    a->out_f32 = (p->flags & PA_DECODE_OUT_F32) || p->q_dtype == PA_F32 ? 1 : 0;
+    a->wait_ns = kWaitLimitNs;
+    return PA_OK;
+}
+
+}  // namespace pa
+
+extern "C" {
+
+int pa_decode_selected(void *out, const void *q, const void *key_cache, const void *value_cache,
+                       const int32_t *block_tables, const int32_t *seq_lens, const int32_t *selected,
+                       const int32_t *num_selected, float scale, const pa_sparse_params *p, pa_stream_t stream) {
+    SparseArgs a;
+    int rc = sparse_args(p, &a);
+    if (rc != PA_OK) return rc;
+    if (a.rows == 0) return PA_OK;
+    rc = attend_args(p, &a, out, q, key_cache, value_cache, block_tables, seq_lens, const_cast<int32_t *>(selected),
+                     const_cast<int32_t *>(num_selected), scale);
+    if (rc != PA_OK) return rc;
+    return launch_decode_selected(a, (cudaStream_t)stream);
+}
+
+int pa_decode_sparse(void *out, const void *q, const void *key_cache, const void *value_cache, const int8_t *bounds,
+                     const float *bound_scales, const int32_t *block_tables, const int32_t *seq_lens, int32_t *selected,
+                     int32_t *num_selected, float scale, const pa_sparse_params *p, pa_stream_t stream) {
+    SparseArgs a;
+    int rc = sparse_args(p, &a);
+    if (rc != PA_OK) return rc;
+    if (a.rows == 0) return PA_OK;
+    if (!bounds || !bound_scales) return PA_ERR_NULL;
+    if ((uintptr_t)bounds % 16) return PA_ERR_ALIGN;
+    rc = attend_args(p, &a, out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, scale);
+    if (rc != PA_OK) return rc;
+    a.bounds = bounds;
+    a.bscales = bound_scales;
+    rc = launch_select_blocks(a, (cudaStream_t)stream);
+    return rc != PA_OK ? rc : launch_decode_selected(a, (cudaStream_t)stream);
+}
+
 int pa_get_error_flags(unsigned int *flags, int reset, pa_stream_t stream) {
     if (!flags) return PA_ERR_NULL;
     if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return PA_ERR_CUDA;
     int (*const words[])(unsigned int *, bool) = {error_word_cache_ops, error_word_decode_simt,
                                                   error_word_decode_tc, error_word_decode_umma,
-                                                  error_word_step_tables, error_word_sparse_select};
+                                                  error_word_step_tables, error_word_sparse_select,
+                                                  error_word_sparse_decode};
     unsigned int all = 0;
     for (auto w : words) {
         unsigned int f = 0;

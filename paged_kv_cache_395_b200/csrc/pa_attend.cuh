@@ -1,0 +1,603 @@
+// Attention of one (query row, KV head) over its chosen blocks, as device code: the whole of
+// pa_decode_selected and the second half of pa_decode_sparse.
+//
+//   out[g] = sum_t softmax_t(scale q[g] . K[t]) V[t] over the tokens t of the chosen blocks
+//
+// A cluster of CTAs shares a row: the chosen blocks go round its warps.  Every warp works
+// alone on its blocks, with its own ring of (K tile, V tile) stages that TMA fills (one copy
+// per tile: a block's tile of one KV head is contiguous), a running maximum and sum per head,
+// and its share of the output in registers; the shares are joined once at the end, first the
+// CTA's warps through shared memory, then the cluster's CTAs through distributed shared
+// memory.  So a row needs no workspace and one launch, and the order of every sum is fixed.
+//
+// Tensor-core form (mma.sync m16n8k16, 8 heads per n-tile, NT n-tiles):
+//   S^T[16 tokens x heads] = K[16 x D] . Q^T[D x heads]     (A = K tile, B = q)
+//   O^T[D x heads]        += V^T[D x 16] . P^T[16 x heads]  (A = V tile^T, B = p)
+// so the accumulators of up to 8 heads take D / 4 registers, and every tile is read from
+// shared memory once for all heads.  bf16 rounds P to 8 bits, too few for the result's own
+// precision, so there P = hi + lo, two products; fp16's 11 bits are enough.  An int8 tile's
+// codes become exact fp16 / bf16 fragments in registers; the block's K scale multiplies the
+// scores, its V scale the block's product, in fp32.
+#pragma once
+#include <cooperative_groups.h>
+
+#include <type_traits>
+
+#include "pa_mma.cuh"
+#include "pa_select.cuh"
+#include "pa_tc_shared.cuh"
+
+namespace pa {
+
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap *map, int tile, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %2, %3}], [%4];" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(tile), "r"(bar)
+        : "memory");
+}
+
+// Bytes b0, b1 of u (int8 values biased by 128) as an exact pair of T.
+template <typename T>
+__device__ __forceinline__ uint32_t i8_pair(uint32_t u, int b0, int b1) {
+    if constexpr (std::is_same<T, __half>::value) {
+        return i8x2_to_h2(u, 0x5040u | (uint32_t)(b1 << 8) | (uint32_t)b0);
+    } else {
+        // 0x4b0000xx is 2^23 + xx: subtracting 2^23 + 128 leaves the value, which bf16's 8 bits hold
+        const float lo = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540u | (uint32_t)b0)) - 8388736.f;
+        const float hi = __uint_as_float(__byte_perm(u, 0x4b000000u, 0x7540u | (uint32_t)b1)) - 8388736.f;
+        return Mma<T>::pack(lo, hi);
+    }
+}
+
+// Shared-memory layout of the tensor-core form.
+template <typename T, typename TKV, int D, int NT>
+struct AttendCfg {
+    static constexpr bool I8 = std::is_same<TKV, int8_t>::value;
+    static constexpr int NW = 4;                                       // warps
+    static constexpr int ROWB = D * (int)sizeof(TKV);                  // bytes per cache row
+    static constexpr int SEGB = ROWB < 128 ? ROWB : 128;               // bytes per box row
+    static constexpr int TILE = 16 * ROWB;
+    static constexpr int STAGE = 2 * TILE;
+    static constexpr int S = STAGE >= 16384 ? 2 : STAGE >= 8192 ? 3 : STAGE >= 4096 ? 4 : 6;  // stages per warp
+    static constexpr int HEADS = NT * 8;
+    static constexpr int QROW = D * 2 + 16;                            // bytes: rows fall into different banks
+    static constexpr int OROW = D + 4;                                 // floats
+    static constexpr int RING = NW * S * STAGE;
+    static constexpr int JOIN = NW * HEADS * OROW * 4;                 // the joining reuses the ring
+    static constexpr int Q_OFF = RING > JOIN ? RING : JOIN;
+    static constexpr int BAR_OFF = Q_OFF + HEADS * QROW;
+    static constexpr int INFO_OFF = BAR_OFF + NW * S * 8;              // int [NW][S]: tokens of the stage's block, 0: none
+    static constexpr int SC_OFF = INFO_OFF + NW * S * 4;               // float [NW][S][2]: int8 K, V scales
+    static constexpr int ML_OFF = SC_OFF + NW * S * 8;                 // float [NW][2][HEADS], then [2][HEADS]
+    static constexpr int BYTES = 1024 + ML_OFF + (NW + 1) * 2 * HEADS * 4;
+    static constexpr bool QREG = NT * D <= 256;                        // q fragments kept in registers
+};
+
+// Joins the warps' and the CTAs' shares and writes the output.  o: float [NW][HEADS][OROW] shares of
+// the CTA's warps, ml: float [NW][2][HEADS] their maxima and sums, then [2][HEADS] for the CTA's own.
+template <typename T, int D, int HEADS, int OROW, int NW>
+__device__ __forceinline__ void join_shares(const SparseArgs &a, float *o, float *ml, int ncol, size_t out0, int rank,
+                                            int ncta) {
+    const int tid = threadIdx.x, nt = NW * 32;
+    float *mine = ml + NW * 2 * HEADS;
+    __syncthreads();
+    if (tid < HEADS) {
+        float M = __int_as_float(0xff800000), l = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * 2 * HEADS + tid]);
+        const float Mu = M == __int_as_float(0xff800000) ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = fast_exp2(ml[w * 2 * HEADS + tid] - Mu);
+            l += f * ml[w * 2 * HEADS + HEADS + tid];
+            ml[w * 2 * HEADS + tid] = f;
+        }
+        mine[tid] = M;
+        mine[HEADS + tid] = l;
+    }
+    __syncthreads();
+    if (ncta == 1) {
+        for (int i = tid; i < ncol * (D / 2); i += nt) {
+            const int g = i / (D / 2), d = i % (D / 2) * 2;
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float f = ml[w * 2 * HEADS + g];
+                const float2 v = *reinterpret_cast<const float2 *>(o + (w * HEADS + g) * OROW + d);
+                x += f * v.x;
+                y += f * v.y;
+            }
+            const float l = mine[HEADS + g], inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+            store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, x * inv, y * inv);
+        }
+        return;
+    }
+    for (int i = tid; i < ncol * (D / 2); i += nt) {
+        const int g = i / (D / 2), d = i % (D / 2) * 2;
+        float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const float f = ml[w * 2 * HEADS + g];
+            const float2 v = *reinterpret_cast<const float2 *>(o + (w * HEADS + g) * OROW + d);
+            s.x += f * v.x;
+            s.y += f * v.y;
+        }
+        *reinterpret_cast<float2 *>(o + g * OROW + d) = s;
+    }
+    cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+    cl.sync();
+    // CTA `rank` writes the pairs rank, rank + ncta, ... of the row's output
+    for (int i = rank * nt + tid; i < ncol * (D / 2); i += ncta * nt) {
+        const int g = i / (D / 2), d = i % (D / 2) * 2;
+        float M = __int_as_float(0xff800000), l = 0.f, x = 0.f, y = 0.f;
+        for (int r = 0; r < ncta; ++r) M = fmaxf(M, *cl.map_shared_rank(mine + g, r));
+        if (M == __int_as_float(0xff800000)) M = 0.f;
+        for (int r = 0; r < ncta; ++r) {
+            const float f = fast_exp2(*cl.map_shared_rank(mine + g, r) - M);
+            l += f * *cl.map_shared_rank(mine + HEADS + g, r);
+            const float2 v = *cl.map_shared_rank(reinterpret_cast<float2 *>(o + g * OROW + d), r);
+            x += f * v.x;
+            y += f * v.y;
+        }
+        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, x * inv, y * inv);
+    }
+    cl.sync();  // no CTA ends while another reads its shares
+}
+
+// The chosen blocks [n_sel] of row r and KV head h, 8 * NT query heads from 8 * NT * grp on.
+// smem: 1024-byte aligned, AttendCfg bytes.  Called by NW * 32 threads of each CTA.
+template <typename T, typename TKV, int D, int NT>
+__device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CUtensorMap *tmV, int r, int h, int grp,
+                           int rank, int ncta, unsigned char *smem) {
+    using C = AttendCfg<T, TKV, D, NT>;
+    constexpr int NW = C::NW, S = C::S, KS = D / 16, MT = D / 16;
+    constexpr bool SPLIT_P = !std::is_same<T, __half>::value;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    const uint32_t sb = smem_addr(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF) + warp * S;
+    int *info = reinterpret_cast<int *>(smem + C::INFO_OFF) + warp * S;
+    float *scs = reinterpret_cast<float *>(smem + C::SC_OFF) + warp * S * 2;
+    const uint32_t ring = sb + warp * S * C::STAGE;
+
+    int b;
+    const int L = sparse_row_len(a, r, b), nb = (L + kBlockSize - 1) / kBlockSize;
+    const size_t list = (size_t)r * a.H + h;
+    const int n = min(max(__ldcg(a.nsel + list), 0), a.K);
+    const int32_t *sel = a.sel + list * a.K, *table = a.tables + (size_t)b * a.M;
+    const int W = ncta * NW, w = rank * NW + warp, cnt = n > w ? (n - w + W - 1) / W : 0;
+
+    // ---- the warp's blocks: lane l of a batch of 32 holds the l-th ----
+    int p_j = 0, p_y = -1;
+    float p_ks = 0.f, p_vs = 0.f;
+    auto batch = [&](int k) {  // items k .. k + 31
+        p_y = -1;
+        if (k + lane < cnt) {
+            p_j = __ldcg(sel + (size_t)(k + lane) * W + w);
+            if (p_j >= 0 && p_j < nb) {  // entries outside the row's blocks are skipped
+                const int x = table[p_j];
+                if (x >= 0 && (int64_t)x < a.N) {
+                    p_y = x * a.H + h;  // host: num_blocks * H below 2^31
+                    if constexpr (C::I8) {
+                        p_ks = a.ks[p_y];
+                        p_vs = a.vs[p_y];
+                    }
+                } else {
+                    raise_flag(PA_EFLAG_BAD_BLOCK);
+                }
+            }
+        }
+    };
+    auto issue = [&](int k) {
+        if (k >= cnt) return;
+        if (k % 32 == 0) batch(k);
+        const int y = __shfl_sync(0xffffffffu, p_y, k % 32), j = __shfl_sync(0xffffffffu, p_j, k % 32);
+        float ks = 0.f, vs = 0.f;
+        if constexpr (C::I8) {
+            ks = __shfl_sync(0xffffffffu, p_ks, k % 32);
+            vs = __shfl_sync(0xffffffffu, p_vs, k % 32);
+        }
+        if (lane == 0) {
+            const int s = k % S;
+            info[s] = y >= 0 ? min(kBlockSize, L - j * kBlockSize) : 0;
+            if constexpr (C::I8) {
+                scs[2 * s] = ks;
+                scs[2 * s + 1] = vs;
+            }
+            if (y >= 0) {
+                mbar_arrive_expect_tx(&bars[s], C::STAGE);
+                tma_tile(ring + s * C::STAGE, tmK, y, smem_addr(&bars[s]));
+                tma_tile(ring + s * C::STAGE + C::TILE, tmV, y, smem_addr(&bars[s]));
+            } else {
+                mbar_arrive(&bars[s]);
+            }
+        }
+        __syncwarp();
+    };
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < S; ++k) issue(k);
+
+    // ---- q: rows of 8 * NT heads, zeros past the group ----
+    const int ncol = min(C::HEADS, a.G - grp * C::HEADS);
+    const size_t row0 = ((size_t)r * a.Hq + (size_t)h * a.G + (size_t)grp * C::HEADS) * D;
+    {
+        uint16_t *qd = reinterpret_cast<uint16_t *>(smem + C::Q_OFF);
+        const uint16_t *qsrc = reinterpret_cast<const uint16_t *>(a.q) + row0;
+        for (int i = tid; i < C::HEADS * D; i += NW * 32) {
+            const int hd = i / D, d = i % D;
+            qd[hd * (C::QROW / 2) + d] = hd < ncol ? qsrc[i] : (uint16_t)0;
+        }
+    }
+    __syncthreads();
+    // B fragment of k-step ks, n-tile nt: the dims in the order of the K fragments
+    auto qfrag = [&](int nt, int ks, uint32_t &b0, uint32_t &b1) {
+        const uint32_t row = sb + C::Q_OFF + (nt * 8 + g) * C::QROW;
+        if constexpr (!C::I8) {
+            b0 = lds_u32(row + (ks * 16 + 2 * c) * 2);
+            b1 = lds_u32(row + (ks * 16 + 2 * c + 8) * 2);
+        } else {
+            // thread column c reads 32 (D = 64: 16) contiguous bytes per 128-byte segment of a row
+            const int d0 = D == 64 ? c * 16 + ks * 4 : (ks / 8) * 128 + c * 32 + (ks % 8) * 4;
+            uint32_t v[2];
+            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(row + d0 * 2) : "memory");
+            b0 = v[0];
+            b1 = v[1];
+        }
+    };
+    uint32_t qb[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
+    if constexpr (C::QREG) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) qfrag(t, ks, qb[t][ks][0], qb[t][ks][1]);
+    }
+
+    float o[NT][MT][4] = {};
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        m[t][0] = m[t][1] = __int_as_float(0xff800000);
+        l[t][0] = l[t][1] = 0.f;
+    }
+
+    for (int k = 0; k < cnt; ++k) {
+        const int s = k % S;
+        // (the lanes give up together)
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (k / S) & 1, a.wait_ns))) {
+            // give up: the copies still in flight are waited for (again with a limit), so that
+            // none lands in memory that the joining reuses
+            for (int i = 1; i < S && k + i < cnt; ++i) mbar_wait(&bars[(k + i) % S], ((k + i) / S) & 1, a.wait_ns);
+            break;
+        }
+        __syncwarp();
+        const int valid = info[s];
+        const uint32_t kt = ring + s * C::STAGE, vt = kt + C::TILE;
+        if (valid > 0) {
+            // ---- S^T ----
+            float x[NT][4];
+            {
+                float acc[2][NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[0][t][e] = acc[1][t][e] = 0.f;
+                if constexpr (!C::I8) {
+                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        uint32_t af[4];
+                        const int ch = ks * 2 + (lane >> 4);
+                        ldsm_x4(af, swz(kt + (ch >> 3) * 2048, row, ch & 7));
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            uint32_t b0, b1;
+                            if constexpr (C::QREG) {
+                                b0 = qb[t][ks][0];
+                                b1 = qb[t][ks][1];
+                            } else {
+                                qfrag(t, ks, b0, b1);
+                            }
+                            Mma<T>::mma(acc[ks & 1][t], af, b0, b1);
+                        }
+                    }
+                } else {
+                    constexpr int V = D == 64 ? 1 : 2;  // 16-byte vectors per thread and segment
+#pragma unroll
+                    for (int sg = 0; sg < (D == 64 ? 1 : D / 128); ++sg) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            uint32_t wa[4], wb[4];
+                            if constexpr (D == 64) {
+                                lds_v4(wa, kt + g * 64 + c * 16);
+                                lds_v4(wb, kt + (g + 8) * 64 + c * 16);
+                            } else {
+                                lds_v4(wa, swz(kt + sg * 2048, g, 2 * c + v));
+                                lds_v4(wb, swz(kt + sg * 2048, g + 8, 2 * c + v));
+                            }
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int ks = sg * 8 + v * 4 + u;
+                                const uint32_t ua = wa[u] ^ 0x80808080u, ub = wb[u] ^ 0x80808080u;
+                                const uint32_t af[4] = {i8_pair<T>(ua, 0, 1), i8_pair<T>(ub, 0, 1), i8_pair<T>(ua, 2, 3),
+                                                        i8_pair<T>(ub, 2, 3)};
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) {
+                                    uint32_t b0, b1;
+                                    if constexpr (C::QREG) {
+                                        b0 = qb[t][ks][0];
+                                        b1 = qb[t][ks][1];
+                                    } else {
+                                        qfrag(t, ks, b0, b1);
+                                    }
+                                    Mma<T>::mma(acc[ks & 1][t], af, b0, b1);
+                                }
+                            }
+                        }
+                    }
+                }
+                const float sc = C::I8 ? a.scale_log2 * scs[2 * s] : a.scale_log2;
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        // rows past the last token hold anything, NaN among it
+                        const bool in = g + 8 * (e >> 1) < valid;
+                        x[t][e] = in ? (acc[0][t][e] + acc[1][t][e]) * sc : __int_as_float(0xff800000);
+                    }
+            }
+            // ---- running maximum and sum; P ----
+            uint32_t ph[NT][2], pl[NT][2];
+            bool moved = false;
+            float al[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(x[t][e], x[t][2 + e]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    const float mn = fmaxf(m[t][e], mx);
+                    const float mu = mn == __int_as_float(0xff800000) ? 0.f : mn;
+                    al[t][e] = fast_exp2(m[t][e] - mu);
+                    moved |= mn != m[t][e];
+                    m[t][e] = mn;
+                    x[t][e] = fast_exp2(x[t][e] - mu);
+                    x[t][2 + e] = fast_exp2(x[t][2 + e] - mu);
+                    l[t][e] = l[t][e] * al[t][e] + (x[t][e] + x[t][2 + e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // tokens g (e = 0) and g + 8, heads 2c, 2c + 1
+                    const uint32_t hi = Mma<T>::pack(x[t][2 * e], x[t][2 * e + 1]);
+                    ph[t][e] = movm_t(hi);
+                    if constexpr (SPLIT_P) {
+                        const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
+                        pl[t][e] = movm_t(Mma<T>::pack(x[t][2 * e] - h0, x[t][2 * e + 1] - h1));
+                    }
+                }
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[t][i][e] *= al[t][e & 1];
+            }
+            // ---- O^T ----
+            if constexpr (!C::I8) {
+                if (valid < kBlockSize) {
+                    // values behind the last token: a weight of 0 does not make a NaN there 0
+                    for (int i = lane; i < (kBlockSize - valid) * (C::ROWB / 16); i += 32) {
+                        const int row = valid + i / (C::ROWB / 16), ch = i % (C::ROWB / 16);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(swz(vt + (ch >> 3) * 2048, row, ch & 7)),
+                                     "r"(0)
+                                     : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const int row = (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    uint32_t af[4];
+                    const int ch = i * 2 + ((lane >> 3) & 1);
+                    ldsm_x4_t(af, swz(vt + (ch >> 3) * 2048, row, ch & 7));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        Mma<T>::mma(o[t][i], af, ph[t][0], ph[t][1]);
+                        if constexpr (SPLIT_P) Mma<T>::mma(o[t][i], af, pl[t][0], pl[t][1]);
+                    }
+                }
+            } else {
+                const float vs = scs[2 * s + 1];
+                constexpr int MS = D == 64 ? 4 : 8, VW = D == 64 ? 2 : 4;  // m-tiles and words per segment
+#pragma unroll
+                for (int sg = 0; sg < MT / MS; ++sg) {
+                    uint32_t rw[4][4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int row = 2 * c + (q & 1) + 8 * (q >> 1);
+                        if constexpr (D == 64) {
+                            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                                         : "=r"(rw[q][0]), "=r"(rw[q][1])
+                                         : "r"(vt + row * 64 + g * 8)
+                                         : "memory");
+                        } else {
+                            lds_v4(rw[q], swz(vt + sg * 2048, row, g));
+                        }
+#pragma unroll
+                        for (int e = 0; e < VW; ++e) rw[q][e] ^= 0x80808080u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < MS; ++i) {
+                        uint32_t af[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // token pair q / 2, dims row (q & 1 ? g + 8 : g)
+                            const int p = q >> 1, wd = (q & 1) * (VW / 2) + i / 4;
+                            const uint32_t sl = (uint32_t)(i & 3) | (uint32_t)(4 + (i & 3)) << 4;
+                            af[q] = i8_pair<T>(__byte_perm(rw[2 * p][wd], rw[2 * p + 1][wd], sl), 0, 1);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            float d[4];
+                            Mma<T>::mma0(d, af, ph[t][0], ph[t][1]);
+                            if constexpr (SPLIT_P) Mma<T>::mma(d, af, pl[t][0], pl[t][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[t][sg * MS + i][e] += vs * d[e];
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        issue(k + S);
+    }
+
+    // ---- this warp's share, then the joining ----
+    float *os = reinterpret_cast<float *>(smem);
+    float *ml = reinterpret_cast<float *>(smem + C::ML_OFF);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
+            if (g == 0) {
+                ml[warp * 2 * C::HEADS + t * 8 + 2 * c + e] = m[t][e];
+                ml[(warp * 2 + 1) * C::HEADS + t * 8 + 2 * c + e] = l[t][e];
+            }
+        }
+    __syncthreads();  // every ring is empty: the shares go there
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                int d;
+                if constexpr (!C::I8)
+                    d = i * 16 + g + 8 * (e >> 1);
+                else if constexpr (D == 64)
+                    d = g * 8 + i + 4 * (e >> 1);
+                else
+                    d = (i / 8) * 128 + g * 16 + i % 8 + 8 * (e >> 1);
+                os[(warp * C::HEADS + t * 8 + 2 * c + (e & 1)) * C::OROW + d] = o[t][i][e];
+            }
+    join_shares<T, D, C::HEADS, C::OROW, NW>(a, os, ml, ncol, row0, rank, ncta);
+}
+
+// fp32 caches: the same on the CUDA cores, GT query heads at a time, tiles read from global
+// memory.  Lane (token t = lane % 16, half = lane / 16) takes half of the dims of its token's
+// product; the output's dims go over the lanes.
+template <int D, int GT>
+struct AttendF32Cfg {
+    static constexpr int NW = 4, OROW = D + 4;
+    static constexpr int Q_OFF = NW * GT * OROW * 4;
+    static constexpr int ML_OFF = Q_OFF + GT * D * 4;
+    static constexpr int BYTES = ML_OFF + (NW + 1) * 2 * GT * 4;
+};
+
+template <int D, int GT>
+__device__ void attend_row_f32(const SparseArgs &a, int r, int h, int grp, int rank, int ncta, unsigned char *smem) {
+    using C = AttendF32Cfg<D, GT>;
+    constexpr int NW = C::NW, DL = D / 32, VL = DL < 4 ? DL : 4;  // dims per lane, per vector
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float *os = reinterpret_cast<float *>(smem), *qs = reinterpret_cast<float *>(smem + C::Q_OFF),
+          *ml = reinterpret_cast<float *>(smem + C::ML_OFF);
+    int b;
+    const int L = sparse_row_len(a, r, b), nb = (L + kBlockSize - 1) / kBlockSize;
+    const size_t list = (size_t)r * a.H + h;
+    const int n = min(max(__ldcg(a.nsel + list), 0), a.K);
+    const int32_t *sel = a.sel + list * a.K, *table = a.tables + (size_t)b * a.M;
+    const int ncol = min(GT, a.G - grp * GT);
+    const size_t row0 = ((size_t)r * a.Hq + (size_t)h * a.G + (size_t)grp * GT) * D;
+    for (int i = tid; i < GT * D; i += NW * 32)
+        qs[i] = i < ncol * D ? reinterpret_cast<const float *>(a.q)[row0 + i] : 0.f;
+    __syncthreads();
+    float o[GT][DL] = {}, m[GT], l[GT];
+#pragma unroll
+    for (int t = 0; t < GT; ++t) {
+        m[t] = __int_as_float(0xff800000);
+        l[t] = 0.f;
+    }
+    const int tok = lane & 15, half = lane >> 4;
+    for (int i = rank * NW + warp; i < n; i += ncta * NW) {
+        const int j = __ldcg(sel + i);
+        if (j < 0 || j >= nb) continue;
+        const int x = table[j];
+        if (x < 0 || (int64_t)x >= a.N) {
+            if (lane == 0) raise_flag(PA_EFLAG_BAD_BLOCK);
+            continue;
+        }
+        const int valid = min(kBlockSize, L - j * kBlockSize);
+        const size_t tile = ((size_t)x * a.H + h) * (kBlockSize * D);
+        const float4 *kp = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.kc) + tile + tok * D + half * (D / 2));
+        float s[GT] = {};
+#pragma unroll 8
+        for (int v = 0; v < D / 8; ++v) {
+            const float4 k4 = __ldg(kp + v);
+#pragma unroll
+            for (int t = 0; t < GT; ++t) {
+                const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * D + half * (D / 2) + 4 * v);
+                s[t] += k4.x * q4.x + k4.y * q4.y + k4.z * q4.z + k4.w * q4.w;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < GT; ++t) {
+            s[t] += __shfl_xor_sync(0xffffffffu, s[t], 16);
+            s[t] = tok < valid ? s[t] * a.scale_log2 : __int_as_float(0xff800000);
+            float mx = s[t];
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+            const float mn = fmaxf(m[t], mx), mu = mn == __int_as_float(0xff800000) ? 0.f : mn;
+            const float al = fast_exp2(m[t] - mu);
+            m[t] = mn;
+            s[t] = fast_exp2(s[t] - mu);
+            l[t] = l[t] * al + (half ? 0.f : s[t]);
+#pragma unroll
+            for (int e = 0; e < DL; ++e) o[t][e] *= al;
+        }
+        const float *vp = reinterpret_cast<const float *>(a.vc) + tile;
+#pragma unroll 4
+        for (int u = 0; u < valid; ++u) {  // only the tokens that are there: what lies behind may be NaN
+            float v[DL];
+#pragma unroll
+            for (int e = 0; e < DL; e += VL) {
+                const float *p = vp + u * D + e * 32 + lane * VL;
+                if constexpr (VL == 4) {
+                    const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
+                    v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
+                } else {
+                    const float2 f = __ldg(reinterpret_cast<const float2 *>(p));
+                    v[e] = f.x, v[e + 1] = f.y;
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < GT; ++t) {
+                const float p = __shfl_sync(0xffffffffu, s[t], u);
+#pragma unroll
+                for (int e = 0; e < DL; ++e) o[t][e] += p * v[e];
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < GT; ++t) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) l[t] += __shfl_xor_sync(0xffffffffu, l[t], d);
+        if (lane == 0) {
+            ml[warp * 2 * GT + t] = m[t];
+            ml[(warp * 2 + 1) * GT + t] = l[t];
+        }
+#pragma unroll
+        for (int e = 0; e < DL; ++e) os[(warp * GT + t) * C::OROW + (e / VL) * 32 * VL + lane * VL + e % VL] = o[t][e];
+    }
+    join_shares<float, D, GT, C::OROW, NW>(a, os, ml, ncol, row0, rank, ncta);
+}
+
+}  // namespace pa

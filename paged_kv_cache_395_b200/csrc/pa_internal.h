@@ -129,8 +129,17 @@ struct SparseArgs {
     int64_t N;
     int max_len;  // effective bound on lengths
     int q_dtype, kv_dtype;
+    // attention
+    void *out;
+    const void *kc, *vc;
+    const float *ks, *vs;
+    float scale_log2;  // scale * log2(e): scores are kept in the log2 domain
+    int out_f32;       // out is fp32: PA_DECODE_OUT_F32, or q is
+    int ng;            // groups of query heads per KV head that run apart
+    unsigned long long wait_ns;  // limit of every bounded wait on a copy
 };
 int launch_select_blocks(const SparseArgs &a, cudaStream_t st);
+int launch_decode_selected(const SparseArgs &a, cudaStream_t st);
 
 // Per-translation-unit error words (see PA_ERROR_WORD_ACCESSOR).
 int error_word_cache_ops(unsigned int *flags, bool reset);
@@ -139,6 +148,7 @@ int error_word_decode_tc(unsigned int *flags, bool reset);
 int error_word_decode_umma(unsigned int *flags, bool reset);
 int error_word_step_tables(unsigned int *flags, bool reset);
 int error_word_sparse_select(unsigned int *flags, bool reset);
+int error_word_sparse_decode(unsigned int *flags, bool reset);
 
 // Raise a kernel's dynamic shared-memory limit on the current device, once per
 // (kernel, device).  Thread-safe; returns false if CUDA refuses.

@@ -1,0 +1,150 @@
+// pa_decode_selected: decode attention over chosen blocks (pa_attend.cuh).
+#include "pa_attend.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace pa {
+
+PA_ERROR_WORD_ACCESSOR(error_word_sparse_decode)
+
+namespace {
+
+// One cluster per (query row, KV head, group of 8 * NT query heads).
+template <typename T, typename TKV, int D, int NT>
+__global__ void __launch_bounds__(128) attend_kernel(const __grid_constant__ CUtensorMap tmK,
+                                                     const __grid_constant__ CUtensorMap tmV, const SparseArgs a) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tmK);
+        prefetch_tensormap(&tmV);
+    }
+    pdl_wait();
+    pdl_release_dependents();
+    cg::cluster_group cl = cg::this_cluster();
+    const int ncta = (int)cl.num_blocks();
+    const int64_t item = blockIdx.x / ncta;
+    const int grp = (int)(item % a.ng);
+    const int64_t rh = item / a.ng;
+    attend_row<T, TKV, D, NT>(a, &tmK, &tmV, (int)(rh / a.H), (int)(rh % a.H), grp, (int)cl.block_rank(), ncta, smem);
+}
+
+template <int D, int GT>
+__global__ void __launch_bounds__(128) attend_f32_kernel(const SparseArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    pdl_wait();
+    pdl_release_dependents();
+    cg::cluster_group cl = cg::this_cluster();
+    const int ncta = (int)cl.num_blocks();
+    const int64_t item = blockIdx.x / ncta;
+    const int grp = (int)(item % a.ng);
+    const int64_t rh = item / a.ng;
+    attend_row_f32<D, GT>(a, (int)(rh / a.H), (int)(rh % a.H), grp, (int)cl.block_rank(), ncta, smem);
+}
+
+// CTAs per row: as many as fill the GPU, each warp with at least two blocks.
+int cluster_of(int64_t items, int K) {
+    int c = 1;
+    while (c < 8 && items * c * 2 <= 2 * 148 && K / (2 * c * 4) >= 2) c *= 2;
+    return c;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), int64_t ctas, int c, int threads, size_t smem, cudaStream_t st,
+                           Args &&...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = c;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+}
+
+// Map over a cache as tiles of [16 rows][D], one copy per tile: box (128 bytes of a row, 16 rows,
+// the row's 128-byte segments, 1 tile), 128-byte swizzle (64-byte int8 rows at D = 64: none).
+bool tile_map(CUtensorMap *m, const void *base, int64_t tiles, int D, int dtype) {
+    auto fn = tc_encode_fn();
+    if (!fn) return false;
+    const int es = dtype == PA_I8 ? 1 : 2, rowb = D * es, segb = rowb < 128 ? rowb : 128;
+    const cuuint64_t dims[4] = {(cuuint64_t)(segb / es), 16, (cuuint64_t)(rowb / segb), (cuuint64_t)tiles};
+    const cuuint64_t strides[3] = {(cuuint64_t)rowb, (cuuint64_t)segb, (cuuint64_t)rowb * 16};
+    const cuuint32_t box[4] = {(cuuint32_t)(segb / es), 16, (cuuint32_t)(rowb / segb), 1};
+    const cuuint32_t es1[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType dt = dtype == PA_I8     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return fn(m, dt, 4, const_cast<void *>(base), dims, strides, box, es1, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              segb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, typename TKV, int D, int NT>
+int launch_attend_t(SparseArgs a, cudaStream_t st) {
+    using C = AttendCfg<T, TKV, D, NT>;
+    a.ng = (a.G + C::HEADS - 1) / C::HEADS;
+    const int64_t items = (int64_t)a.rows * a.H * a.ng;
+    const int c = cluster_of(items, a.K);
+    auto kern = attend_kernel<T, TKV, D, NT>;
+    if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), C::BYTES)) return PA_ERR_CUDA;
+    CUtensorMap tk, tv;
+    if (!tile_map(&tk, a.kc, a.N * a.H, D, a.kv_dtype) || !tile_map(&tv, a.vc, a.N * a.H, D, a.kv_dtype)) return PA_ERR_CUDA;
+    return launch_cluster(kern, items * c, c, C::NW * 32, C::BYTES, st, tk, tv, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <typename T, typename TKV>
+int launch_attend_d(const SparseArgs &a, cudaStream_t st) {
+    // n-tiles of 8 heads: as many as the group has and the registers hold, so that a tile is read
+    // once for all of them
+    switch (a.D) {
+    case 64:
+        return a.G <= 8 ? launch_attend_t<T, TKV, 64, 1>(a, st)
+                        : a.G <= 16 ? launch_attend_t<T, TKV, 64, 2>(a, st) : launch_attend_t<T, TKV, 64, 4>(a, st);
+    case 128:
+        return a.G <= 8 ? launch_attend_t<T, TKV, 128, 1>(a, st)
+                        : a.G <= 16 ? launch_attend_t<T, TKV, 128, 2>(a, st) : launch_attend_t<T, TKV, 128, 4>(a, st);
+    default: return a.G <= 8 ? launch_attend_t<T, TKV, 256, 1>(a, st) : launch_attend_t<T, TKV, 256, 2>(a, st);
+    }
+}
+
+template <int D, int GT>
+int launch_attend_f32_t(SparseArgs a, cudaStream_t st) {
+    using C = AttendF32Cfg<D, GT>;
+    a.ng = (a.G + GT - 1) / GT;
+    const int64_t items = (int64_t)a.rows * a.H * a.ng;
+    const int c = cluster_of(items, a.K);
+    auto kern = attend_f32_kernel<D, GT>;
+    if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), C::BYTES)) return PA_ERR_CUDA;
+    return launch_cluster(kern, items * c, c, C::NW * 32, C::BYTES, st, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <int D>
+int launch_attend_f32_d(const SparseArgs &a, cudaStream_t st) {
+    return a.G == 1   ? launch_attend_f32_t<D, 1>(a, st)
+           : a.G == 2 ? launch_attend_f32_t<D, 2>(a, st)
+           : a.G <= 4 ? launch_attend_f32_t<D, 4>(a, st)
+                      : launch_attend_f32_t<D, 8>(a, st);
+}
+
+}  // namespace
+
+int launch_decode_selected(const SparseArgs &a, cudaStream_t st) {
+    if (a.q_dtype == PA_F32)
+        return a.D == 64    ? launch_attend_f32_d<64>(a, st)
+               : a.D == 128 ? launch_attend_f32_d<128>(a, st)
+                            : launch_attend_f32_d<256>(a, st);
+    if (a.q_dtype == PA_F16)
+        return a.kv_dtype == PA_I8 ? launch_attend_d<__half, int8_t>(a, st) : launch_attend_d<__half, __half>(a, st);
+    return a.kv_dtype == PA_I8 ? launch_attend_d<__nv_bfloat16, int8_t>(a, st)
+                               : launch_attend_d<__nv_bfloat16, __nv_bfloat16>(a, st);
+}
+
+}  // namespace pa

@@ -89,6 +89,8 @@ struct Chunks {
 
 
 // Host side (pa_decode_tc.cu).
+// The driver's tensor-map encoder, looked up once; NULL where the driver has none.
+PFN_cuTensorMapEncodeTiled_v12000 tc_encode_fn();
 // 2-D TMA map over a cache [rows][D] (128-byte boxes of 16 rows, 128-byte swizzle;
 // 4-bit: one unswizzled box per row), cached by (base, rows, D, dtype).
 bool tc_cache_tensor_map(CUtensorMap *m, const void *base, int64_t rows, int D, int dtype);

@@ -6,7 +6,8 @@ The names mirror the C ABI in ``include/pa.h``:
   ``pa_decode_append_fused``, ``pa_decode_fixed_scratch``,
   ``pa_decode_stall_selftest``, ``pa_block_copy``, ``pa_quantize_int8``,
   ``pa_quantize_int4``, ``pa_append_int8``, ``pa_step_tables``,
-  ``pa_block_bounds``, ``pa_select_blocks``, ``pa_decode_workspace_size``,
+  ``pa_block_bounds``, ``pa_select_blocks``, ``pa_decode_selected``, ``pa_decode_sparse``,
+  ``pa_decode_workspace_size``,
   ``pa_decode_algo``, ``pa_get_error_flags`` take torch CUDA tensors (or raw device pointers via ``lib``), check device,
   dtype and contiguity, and call the library on
   ``torch.cuda.current_stream()``.  Every step of the computation runs in the
@@ -115,6 +116,8 @@ def _load():
     L.pa_step_tables.argtypes = [P] * 11 + [i32, i32, i64, i64, i32, P]
     L.pa_block_bounds.argtypes = [P] * 7 + [i32] * 5 + [i64, i64, i32, P]
     L.pa_select_blocks.argtypes = [P] * 7 + [ctypes.POINTER(PaSparseParams), P]
+    L.pa_decode_selected.argtypes = [P] * 8 + [f32, ctypes.POINTER(PaSparseParams), P]
+    L.pa_decode_sparse.argtypes = [P] * 10 + [f32, ctypes.POINTER(PaSparseParams), P]
     L.pa_get_error_flags.argtypes = [ctypes.POINTER(ctypes.c_uint), i32, P]
     L.pa_status_string.argtypes = [i32]
     L.pa_status_string.restype = ctypes.c_char_p
@@ -123,7 +126,7 @@ def _load():
               "pa_decode_append_fused", "pa_decode_fixed_scratch",
               "pa_decode_stall_selftest", "pa_decode_algo", "pa_decode_launches", "pa_block_copy",
               "pa_quantize_int8", "pa_quantize_int4", "pa_step_tables", "pa_block_bounds", "pa_select_blocks",
-              "pa_get_error_flags", "pa_version"):
+              "pa_decode_selected", "pa_decode_sparse", "pa_get_error_flags", "pa_version"):
         getattr(L, n).restype = i32
     return L
 
@@ -134,8 +137,8 @@ lib = _load()
 EXPORTED = ("pa_reshape_and_cache", "pa_reshape_and_cache_ex", "pa_append_int8", "pa_decode_workspace_size",
             "pa_decode_algo", "pa_decode_launches", "pa_decode", "pa_decode_append", "pa_decode_append_fused",
             "pa_decode_fixed_scratch", "pa_decode_stall_selftest", "pa_block_copy", "pa_quantize_int8",
-            "pa_quantize_int4", "pa_step_tables", "pa_block_bounds", "pa_select_blocks", "pa_get_error_flags",
-            "pa_status_string", "pa_version")
+            "pa_quantize_int4", "pa_step_tables", "pa_block_bounds", "pa_select_blocks", "pa_decode_selected",
+            "pa_decode_sparse", "pa_get_error_flags", "pa_status_string", "pa_version")
 FIXED_SCRATCH_BYTES = 32 << 20  # PA_FIXED_SCRATCH_BYTES
 
 
@@ -558,6 +561,50 @@ def pa_select_blocks(selected, num_selected, q, bounds, bound_scales, block_tabl
     _check(lib.pa_select_blocks(selected.data_ptr(), num_selected.data_ptr(), q.data_ptr(), bounds.data_ptr(),
                                 bound_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
                                 ctypes.byref(p), _stream_on(dev, stream)), "pa_select_blocks")
+
+
+def _sparse_decode(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, max_seq_len,
+                   sink_blocks, recent_blocks, k_scales, v_scales):
+    N, H, bs, d = key_cache.shape
+    if value_cache.shape != key_cache.shape or value_cache.dtype != key_cache.dtype or bs != BLOCK_SIZE or \
+            d != q.shape[-1]:
+        raise ValueError("caches must be [N][H_kv][16][d] of one dtype, with q's d")
+    _contiguous(out=out, key_cache=key_cache, value_cache=value_cache, k_scales=k_scales, v_scales=v_scales)
+    for t in (k_scales, v_scales):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (N, H)):
+            raise ValueError("scales must be float32 [N][H_kv]")
+    return _sparse_params(q, H, N, block_tables, seq_lens, selected, num_selected, max_seq_len, sink_blocks,
+                          recent_blocks, dtype_code(key_cache.dtype), k_scales, v_scales, _out_flag(out, q))
+
+
+def pa_decode_selected(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, scale,
+                       max_seq_len, k_scales=None, v_scales=None, stream=None):
+    """Decode attention over the blocks that selected / num_selected list (int32
+    [B][H_kv][K], [B][H_kv], or with a Q after the B; see include/pa.h).  out, q, caches,
+    block_tables and seq_lens as in pa_decode; int8 caches with their scales."""
+    dev = _here(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, k_scales, v_scales)
+    p = _sparse_decode(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, max_seq_len,
+                       0, 1, k_scales, v_scales)
+    _check(lib.pa_decode_selected(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                  block_tables.data_ptr(), seq_lens.data_ptr(), selected.data_ptr(),
+                                  num_selected.data_ptr(), scale, ctypes.byref(p), _stream_on(dev, stream)),
+           "pa_decode_selected")
+
+
+def pa_decode_sparse(out, q, key_cache, value_cache, bounds, bound_scales, block_tables, seq_lens, selected,
+                     num_selected, scale, max_seq_len, sink_blocks=1, recent_blocks=2, k_scales=None, v_scales=None,
+                     stream=None):
+    """pa_select_blocks and pa_decode_selected in one call: selected and num_selected
+    are filled and attended to.  Arguments as in those."""
+    dev = _here(out, q, key_cache, value_cache, bounds, bound_scales, block_tables, seq_lens, selected, num_selected,
+                k_scales, v_scales)
+    p = _sparse_decode(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, max_seq_len,
+                       sink_blocks, recent_blocks, k_scales, v_scales)
+    _boxes(bounds, bound_scales, p.num_blocks, p.num_kv_heads, p.head_dim)
+    _check(lib.pa_decode_sparse(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(),
+                                seq_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), scale,
+                                ctypes.byref(p), _stream_on(dev, stream)), "pa_decode_sparse")
 
 
 def pa_get_error_flags(reset: bool = True, stream=None) -> int:

@@ -1,0 +1,383 @@
+"""pa_decode_selected and pa_decode_sparse: refusals (CPU); attention over chosen blocks
+against the numpy model in 64 bits, the choice of pa_decode_sparse bit for bit, and a
+decode loop of all the step's calls (GPU).
+
+Tolerances (|err| <= atol + rtol |ref|, gpu_util.TOL and its derivation): the fp32 result
+before its rounding to the output type.  fp16 and bf16: products of exact inputs are summed
+in fp32; P is rounded to fp16 (2^-11 of each weight, so at most 2^-11 max|v| < 2.5e-3 / 1 of
+|v| <= 5 in the worst case, and about 2^-11 |v| / sqrt(tokens) on average) or to two bf16
+(2^-17).  A 16-bit output adds half a step of its type: fp16 2^-11 |ref|, inside rtol; bf16
+is checked as an fp32 output and then for being its rounding."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_395_b200 import pa
+from paged_kv_cache_395_b200.block_manager import BlockManager
+
+from . import sparse_model as M
+from .gpu_util import assert_close, bits, check_bf16
+from .test_sparse_select import BAD_SPARSE, paged, sparse_params, to_dev, to_store
+
+BS = 16
+FAKE = 0x1000
+
+
+@pytest.mark.parametrize("kw,status", BAD_SPARSE)
+def test_refusals(kw, status):
+    p = sparse_params(**kw)
+    f = ctypes.c_void_p(FAKE)
+    assert pa.lib.pa_decode_selected(*[f] * 8, 0.1, ctypes.byref(p), None) == status
+    assert pa.lib.pa_decode_sparse(*[f] * 10, 0.1, ctypes.byref(p), None) == status
+
+
+def test_pointers():
+    for fn, n, al in ((pa.lib.pa_decode_selected, 8, (2, 3)), (pa.lib.pa_decode_sparse, 10, (2, 3, 4))):
+        p = sparse_params()
+        assert fn(*[ctypes.c_void_p(FAKE)] * n, 0.1, None, None) == pa.PA_ERR_NULL
+        for i in range(n):
+            args = [ctypes.c_void_p(None if k == i else FAKE) for k in range(n)]
+            assert fn(*args, 0.1, ctypes.byref(p), None) == pa.PA_ERR_NULL
+        for i in al:
+            args = [ctypes.c_void_p(FAKE + 8 * (k == i)) for k in range(n)]
+            assert fn(*args, 0.1, ctypes.byref(p), None) == pa.PA_ERR_ALIGN
+        assert fn(*[None] * n, 0.1, ctypes.byref(sparse_params(num_seqs=0)), None) == pa.PA_OK
+        args = [ctypes.c_void_p(FAKE)] * n
+        assert fn(*args, 0.1, ctypes.byref(sparse_params(kv_dtype=pa.PA_I8)), None) == pa.PA_ERR_NULL  # no scales
+        p = sparse_params(num_blocks=1 << 31, num_kv_heads=2, num_q_heads=2)
+        assert fn(*args, 0.1, ctypes.byref(p), None) == pa.PA_ERR_UNSUPPORTED
+
+
+# ---------------------------------------------------------------------------
+class Case:
+    """A paged cache whose slots past each row's length hold NaN (int8: any code)."""
+
+    def __init__(self, lens, H, G, d, dtype, cache=None, Q=1, seed=0, q_scale=1.0):
+        rng = np.random.default_rng(seed)
+        self.lens, self.H, self.G, self.d, self.dtype, self.Q = lens, H, G, d, dtype, Q
+        self.tables, N = paged(rng, lens)
+        k = rng.standard_normal((N, H, BS, d)) * 0.8 + rng.standard_normal((1, H, 1, d)) * 0.5
+        v = rng.standard_normal((N, H, BS, d))
+        self.ks = self.vs = None
+        if cache == "int8":
+            self.ks = (np.abs(k).max((2, 3)) / 127).astype(np.float32)
+            self.vs = (np.abs(v).max((2, 3)) / 127).astype(np.float32)
+            self.kc = np.rint(k / self.ks[:, :, None, None]).astype(np.int8)
+            self.vc = np.rint(v / self.vs[:, :, None, None]).astype(np.int8)
+            self.kf, self.vf = self.kc, self.vc
+            keys = (self.kc.astype(np.float32) * self.ks[:, :, None, None]).astype(np.float32)
+        else:
+            used = np.zeros((N, BS), bool)
+            for b, n in enumerate(lens):
+                for j in range(-(-max(n, 0) // BS)):
+                    used[self.tables[b, j], :min(BS, n - j * BS)] = True
+            gone = ~used[:, None, :, None] & np.ones(k.shape, bool)
+            k[gone], v[gone] = np.nan, np.nan
+            self.kc, self.vc = to_store(k, dtype), to_store(v, dtype)
+            self.kf, self.vf = M.values(self.kc), M.values(self.vc)
+            keys = self.kf
+        self.codes, self.bs = M.boxes(keys)
+        self.q = to_store(rng.standard_normal((len(lens), Q, H * G, d)) * q_scale, dtype)
+        self.qf = M.values(self.q)
+        self.scale, self.max_len = d ** -0.5, max([1] + list(lens))
+        lead = (len(lens), Q) if Q > 1 else (len(lens),)
+        self.lead = lead
+        self.dev = dict(q=to_dev(self.q, dtype).reshape(lead + (H * G, d)).contiguous(),
+                        kc=to_dev(self.kc, dtype if cache != "int8" else "i"),
+                        vc=to_dev(self.vc, dtype if cache != "int8" else "i"), tables=to_dev(self.tables, "i"),
+                        lens=to_dev(np.array(lens, np.int32), "i"), bounds=to_dev(self.codes, "i"), bs=to_dev(self.bs, "f"),
+                        ks=None if self.ks is None else to_dev(self.ks, "f"),
+                        vs=None if self.vs is None else to_dev(self.vs, "f"))
+
+    def lists(self, K, seed=0, shuffle=False):
+        """Random chosen blocks: sel [B][Q][H][K], counts."""
+        rng = np.random.default_rng(seed)
+        B, H = len(self.lens), self.H
+        sel, cnt = np.full((B, self.Q, H, K), -1, np.int32), np.zeros((B, self.Q, H), np.int32)
+        L = M.row_lens(self.lens, self.Q, self.max_len)
+        for b in range(B):
+            for t in range(self.Q):
+                n = -(-int(L[b, t]) // BS)
+                for h in range(H):
+                    k = min(n, K)
+                    cnt[b, t, h] = k
+                    pick = rng.permutation(n)[:k]
+                    if k and n - 1 not in pick:
+                        pick[0] = n - 1
+                    sel[b, t, h, :k] = pick if shuffle else np.sort(pick)
+        return sel, cnt
+
+    def attend(self, sel, cnt, out_f32=False):
+        d = self.dev
+        K = sel.shape[-1]
+        s = torch.from_numpy(sel).cuda().reshape(self.lead + (self.H, K)).contiguous()
+        c = torch.from_numpy(cnt).cuda().reshape(self.lead + (self.H,)).contiguous()
+        out = torch.full(d["q"].shape, float("nan"), dtype=torch.float32 if out_f32 else d["q"].dtype, device="cuda")
+        pa.pa_decode_selected(out, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], s, c, self.scale, self.max_len,
+                              k_scales=d["ks"], v_scales=d["vs"])
+        return out
+
+    def sparse(self, K, sink, recent, out_f32=False):
+        d = self.dev
+        s = torch.full(self.lead + (self.H, K), 77, dtype=torch.int32, device="cuda")
+        c = torch.full(self.lead + (self.H,), 77, dtype=torch.int32, device="cuda")
+        out = torch.full(d["q"].shape, float("nan"), dtype=torch.float32 if out_f32 else d["q"].dtype, device="cuda")
+        pa.pa_decode_sparse(out, d["q"], d["kc"], d["vc"], d["bounds"], d["bs"], d["tables"], d["lens"], s, c, self.scale,
+                            self.max_len, sink, recent, k_scales=d["ks"], v_scales=d["vs"])
+        return out, s.cpu().numpy().reshape(len(self.lens), self.Q, self.H, K), \
+            c.cpu().numpy().reshape(len(self.lens), self.Q, self.H)
+
+    def model(self, sel, cnt):
+        return M.attend(self.qf, self.kf, self.vf, self.tables, self.lens, sel, cnt, self.scale, self.max_len, self.ks,
+                        self.vs)
+
+    def check(self, got, ref, got32=None, what=""):
+        ref = ref.reshape(got.shape)
+        if self.dtype == "bfloat16":
+            check_bf16(got, got32, ref, what)
+        else:
+            assert_close(got, ref, self.dtype, what)
+
+
+LENS = [0, 1, 15, 16, 17, 31, 160, 333, 1000]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("bfloat16", None), ("float32", None), ("float16", "int8"),
+                                         ("bfloat16", "int8")])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,G", [(2, 1), (8, 4), (1, 5), (2, 8), (1, 16), (1, 20), (1, 64)])
+def test_attention_over_chosen_blocks(dtype, cache, d, H, G):
+    w = Case(LENS, H, G, d, dtype, cache, seed=d + G)
+    pa.pa_get_error_flags(reset=True)
+    for K, shuffle in ((1, False), (9, True), (63, False)):
+        sel, cnt = w.lists(K, K, shuffle)
+        w.check(w.attend(sel, cnt), w.model(sel, cnt), w.attend(sel, cnt, True), f"K={K}")
+    assert pa.pa_get_error_flags(reset=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("bfloat16", None), ("float32", None), ("float16", "int8")])
+@pytest.mark.parametrize("B,L,K", [(1, 5000, 300), (1, 5000, 17), (3, 3000, 64), (40, 700, 30)])
+def test_rows_split_over_ctas(dtype, cache, B, L, K):
+    """From one CTA per row to eight; more blocks per warp than one batch of 32."""
+    w = Case([L + 3 * b for b in range(B)], 2, 4, 128, dtype, cache, seed=L + B)
+    sel, cnt = w.lists(K, 5)
+    w.check(w.attend(sel, cnt), w.model(sel, cnt), w.attend(sel, cnt, True))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
+@pytest.mark.parametrize("Q", [2, 3])
+def test_several_new_tokens(dtype, Q):
+    w = Case([1, 2, 3, 16, 17, 18, 19, 450], 2, 3, 128, dtype, Q=Q, seed=Q)
+    sel, cnt = w.lists(7, Q)
+    w.check(w.attend(sel, cnt), w.model(sel, cnt), w.attend(sel, cnt, True))
+    out, s, c = w.sparse(7, 1, 2)
+    want = M.choose(w.qf, w.codes, w.bs, w.tables, w.lens, 7, 1, 2, w.max_len)
+    assert np.array_equal(s, want[0]) and np.array_equal(c, want[1])
+    w.check(out, w.model(s, c), w.sparse(7, 1, 2, True)[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("bfloat16", None), ("float32", None), ("float16", "int8"),
+                                         ("bfloat16", "int8")])
+@pytest.mark.parametrize("d,H,G,K", [(128, 8, 4, 16), (64, 2, 8, 5), (256, 2, 2, 20), (128, 1, 32, 12), (128, 3, 7, 70)])
+def test_choose_and_attend(dtype, cache, d, H, G, K):
+    w = Case([0, 1, 16, 80, 100, 640, 1023], H, G, d, dtype, cache, seed=K)
+    out, s, c = w.sparse(K, 1, 2)
+    want = M.choose(w.qf, w.codes, w.bs, w.tables, w.lens, K, 1, 2, w.max_len)
+    assert np.array_equal(s, want[0]) and np.array_equal(c, want[1])
+    w.check(out, w.model(s, c), w.sparse(K, 1, 2, True)[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("bfloat16", None), ("float32", None), ("float16", "int8")])
+def test_all_blocks_is_dense_decode(dtype, cache):
+    """With every block chosen the result is pa_decode's, to the two calls' tolerances."""
+    w = Case([1, 40, 333, 1000], 4, 4, 128, dtype, cache, seed=2)
+    out, s, c = w.sparse(63, 1, 1, True)
+    d = w.dev
+    dense = torch.empty_like(out)
+    pa.pa_decode(dense, d["q"], d["kc"], d["vc"], d["tables"], d["lens"], w.scale, w.max_len, d["ks"], d["vs"])
+    tol = 2e-5 if dtype == "float32" else 4e-3
+    assert torch.allclose(out, dense, atol=tol, rtol=tol)
+
+
+@pytest.mark.gpu
+def test_sharp_softmax_and_long_lists():
+    for dtype in ("float16", "bfloat16", "float32"):
+        w = Case([2000, 37], 2, 4, 128, dtype, seed=8, q_scale=8.0)
+        sel, cnt = w.lists(125, 3)
+        # scores up to |q| |k| d^-1/2 ~ 100: fp32 sums of products of that size are off by up to
+        # 128 * 2^-24 * 100 ~ 8e-4 at worst and about 1e-5 in earnest, a relative error of the weights
+        got, ref = w.attend(sel, cnt, True).double().cpu().numpy(), w.model(sel, cnt)
+        assert np.abs(got - ref.reshape(got.shape)).max() < (5e-3 if dtype != "float32" else 1e-3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("float32", None), ("float16", "int8")])
+def test_lists_and_tables_with_bad_entries(dtype, cache):
+    """Entries outside the row are skipped, repeated ones count twice, counts outside [0, K]
+    are cut, table entries outside the pool are skipped and reported."""
+    w = Case([100, 100, 100, 100, 100], 2, 2, 64, dtype, cache, seed=4)
+    sel = np.array([[-1, 2, 7, 6], [3, 3, 1, 0], [2147483647, -2147483648, 4, 4], [0, 1, 2, 3], [5, 0, 0, 0]], np.int32)
+    sel = np.repeat(sel[:, None, None, :], 2, 2).copy()
+    cnt = np.repeat(np.array([4, 3, 3, 99, -5], np.int32)[:, None, None], 2, 2).copy()
+    pa.pa_get_error_flags(reset=True)
+    got = w.attend(sel, cnt)
+    assert pa.pa_get_error_flags(reset=True) == 0
+    ref = w.model(sel, np.clip(cnt, 0, 4))
+    w.check(got, ref)
+    assert (ref[4] == 0).all() and (got[4] == 0).all()
+    w.tables[0, 2], w.tables[1, 3], w.tables[3, 0] = -4, len(w.bs), 2147483647
+    w.dev["tables"] = to_dev(w.tables, "i")
+    got = w.attend(sel, cnt)
+    assert pa.pa_get_error_flags(reset=True) == pa.PA_EFLAG_BAD_BLOCK
+    w.check(got, w.model(sel, np.clip(cnt, 0, 4)))
+
+
+@pytest.mark.gpu
+def test_unaligned_q_and_out():
+    w = Case([100, 333], 2, 4, 128, "float16", seed=6)
+    sel, cnt = w.lists(5)
+    flat = torch.empty(w.dev["q"].numel() + 1, dtype=torch.float16, device="cuda")
+    flat[1:] = w.dev["q"].reshape(-1)
+    out = torch.empty(w.dev["q"].numel() + 1, dtype=torch.float16, device="cuda")
+    q, o = flat[1:].view(w.dev["q"].shape), out[1:].view(w.dev["q"].shape)
+    d = w.dev
+    pa.pa_decode_selected(o, q, d["kc"], d["vc"], d["tables"], d["lens"], torch.from_numpy(sel[:, 0]).cuda().contiguous(),
+                          torch.from_numpy(cnt[:, 0]).cuda().contiguous(), w.scale, w.max_len)
+    assert np.array_equal(bits(o), bits(w.attend(sel, cnt)))
+
+
+@pytest.mark.gpu
+def test_same_result_every_time_and_on_another_stream():
+    w = Case([5000, 4000], 2, 4, 128, "bfloat16", seed=7)
+    out, s, c = w.sparse(100, 1, 2)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        with torch.cuda.stream(st):
+            again, s2, c2 = w.sparse(100, 1, 2)
+        st.synchronize()
+        assert np.array_equal(bits(out), bits(again)) and np.array_equal(s, s2) and np.array_equal(c, c2)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    a, b = Case([3000] * 4, 8, 4, 128, "float16", seed=1), Case([2500] * 5, 4, 8, 128, "float16", seed=2)
+    ra, rb = a.sparse(60, 1, 2)[0], b.sparse(50, 1, 2)[0]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        with torch.cuda.stream(s1):
+            outs.append((a.attend, a.sparse(60, 1, 2)[0], ra))
+        with torch.cuda.stream(s2):
+            outs.append((b.attend, b.sparse(50, 1, 2)[0], rb))
+    torch.cuda.synchronize()
+    for _, got, ref in outs:
+        assert np.array_equal(bits(got), bits(ref))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_sparse_decode_loop(captured):
+    """Tables, append, boxes, choice and attention of a growing batch, eager and as a replayed
+    graph, with requests that end and begin: every step against the host's manager and the
+    numpy model."""
+    B, W, N, H, G, d, K = 6, 12, 120, 2, 4, 64, 5
+    rng = np.random.default_rng(21)
+    bm = BlockManager(N, free_order=rng.permutation(N))
+    ids, nxt, hist = [None] * B, 0, {}
+    dt = torch.float16
+    kc = torch.full((N, H, BS, d), float("nan"), dtype=dt, device="cuda")
+    vc = torch.full_like(kc, float("nan"))
+    bounds, bscales = torch.zeros((N, H, 2, d), dtype=torch.int8, device="cuda"), torch.full((N, H), float("nan"), device="cuda")
+    tables = torch.full((B, W), -1, dtype=torch.int32, device="cuda")
+    lens, before = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    news = torch.zeros(B, dtype=torch.int32, device="cuda")
+    free = torch.tensor(bm._free, dtype=torch.int32, device="cuda")
+    count = torch.tensor([N], dtype=torch.int32, device="cuda")
+    T = 256
+    slots = torch.empty(T, dtype=torch.int64, device="cuda")
+    k, v = torch.zeros((T, H, d), dtype=dt, device="cuda"), torch.zeros((T, H, d), dtype=dt, device="cuda")
+    q, out = torch.zeros((B, H * G, d), dtype=dt, device="cuda"), torch.zeros((B, H * G, d), dtype=dt, device="cuda")
+    sel, nsel = torch.zeros((B, H, K), dtype=torch.int32, device="cuda"), torch.zeros((B, H), dtype=torch.int32, device="cuda")
+
+    def step():
+        before.copy_(lens)
+        before.masked_fill_(news < 0, 0)
+        pa.pa_step_tables(tables, lens, news, free, count, slots)
+        pa.pa_reshape_and_cache(k, v, kc, vc, slots)
+        pa.pa_block_bounds(bounds, bscales, kc, tables, lens, W * BS, first_lens=before)
+        pa.pa_decode_sparse(out, q, kc, vc, bounds, bscales, tables, lens, sel, nsel, d ** -0.5, W * BS, 1, 2)
+
+    graph = None
+    if captured:
+        st = torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            step()  # no tokens yet: warms up
+        st.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            step()
+    pa.pa_get_error_flags(reset=True)
+    for _ in range(60):
+        new = np.zeros(B, np.int32)
+        for b in range(B):
+            if ids[b] is None:
+                new[b] = rng.integers(0, 41)
+            elif rng.random() < 0.05 or bm.lens[ids[b]] == W * BS:
+                new[b] = -1
+            else:
+                new[b] = 1
+        total = int(np.maximum(new, 0).sum())
+        kn, vn = rng.standard_normal((T, H, d)).astype(np.float16), rng.standard_normal((T, H, d)).astype(np.float16)
+        qn = rng.standard_normal((B, H * G, d)).astype(np.float16)
+        news.copy_(torch.from_numpy(new))
+        k.copy_(torch.from_numpy(kn))
+        v.copy_(torch.from_numpy(vn))
+        q.copy_(torch.from_numpy(qn))
+        graph.replay() if captured else step()
+        for b in range(B):
+            if new[b] == -1:
+                bm.free_sequence(ids[b])
+                ids[b] = None
+        want_slots, at = [], 0
+        for b in range(B):
+            if new[b] > 0 and ids[b] is None:
+                want_slots += bm.add_sequence(nxt, int(new[b])).tolist()
+                ids[b], hist[nxt] = nxt, ([], [])
+                nxt += 1
+            elif new[b] > 0:
+                want_slots.append(bm.append_slot(ids[b])[0])
+            if new[b] > 0:
+                hist[ids[b]][0].append(kn[at:at + new[b]])
+                hist[ids[b]][1].append(vn[at:at + new[b]])
+                at += int(new[b])
+        got_slots = slots.cpu().numpy()
+        assert got_slots[:total].tolist() == want_slots and (got_slots[total:] == -1).all()
+        sel_h, cnt_h, out_h = sel.cpu().numpy(), nsel.cpu().numpy(), out.double().cpu().numpy()
+        for b in range(B):
+            n = bm.lens[ids[b]] if ids[b] is not None else 0
+            if n == 0:
+                assert (out_h[b] == 0).all() and (cnt_h[b] == 0).all()
+                continue
+            kk, vv = np.concatenate(hist[ids[b]][0]), np.concatenate(hist[ids[b]][1])
+            nb = -(-n // BS)
+            kp, vp = np.zeros((nb * BS, H, d), np.float32), np.zeros((nb * BS, H, d), np.float32)
+            kp[:n], vp[:n] = kk, vv
+            kp, vp = [x.reshape(nb, BS, H, d).transpose(0, 2, 1, 3) for x in (kp, vp)]
+            codes, s = M.boxes(kp)
+            t = np.arange(nb, dtype=np.int32)[None]
+            qf = qn[b][None, None].astype(np.float32)
+            ws, wc = M.choose(qf, codes, s, t, [n], K, 1, 2, n)
+            assert np.array_equal(ws[0, 0], sel_h[b]) and np.array_equal(wc[0, 0], cnt_h[b])
+            ref = M.attend(qf, kp, vp, t, [n], ws, wc, d ** -0.5, n)[0, 0]
+            assert np.all(np.abs(out_h[b] - ref) <= 2e-3 + 2e-3 * np.abs(ref))
+    assert pa.pa_get_error_flags(reset=True) == 0
