@@ -59,7 +59,11 @@ struct AttendCfg {
     static constexpr int SEGB = ROWB < 128 ? ROWB : 128;               // bytes per box row
     static constexpr int TILE = 16 * ROWB;
     static constexpr int STAGE = 2 * TILE;
-    static constexpr int S = STAGE >= 16384 ? 2 : STAGE >= 8192 ? 3 : STAGE >= 4096 ? 4 : 6;  // stages per warp
+    // Blocks per step: with two, the step's maximum, its exchanges between lanes and the rescaling
+    // are shared by 32 tokens.  The ring holds one step or 16 KB a warp: the warps of several CTAs
+    // on an SM take turns at waiting, so a deeper ring would only cost residency.
+    static constexpr int NB = TILE > 4096 ? 1 : 2;
+    static constexpr int S = STAGE >= 8192 ? 2 : 16384 / STAGE;        // stages per warp
     static constexpr int HEADS = NT * 8;
     static constexpr int QROW = D * 2 + 16;                            // bytes: rows fall into different banks
     static constexpr int OROW = D + 4;                                 // floats
@@ -69,90 +73,119 @@ struct AttendCfg {
     static constexpr int BAR_OFF = Q_OFF + HEADS * QROW;
     static constexpr int INFO_OFF = BAR_OFF + NW * S * 8;              // int [NW][S]: tokens of the stage's block, 0: none
     static constexpr int SC_OFF = INFO_OFF + NW * S * 4;               // float [NW][S][2]: int8 K, V scales
-    static constexpr int ML_OFF = SC_OFF + NW * S * 8;                 // float [NW][2][HEADS], then [2][HEADS]
-    static constexpr int BYTES = 1024 + ML_OFF + (NW + 1) * 2 * HEADS * 4;
+    static constexpr int ML_OFF = SC_OFF + NW * S * 8;                 // float [NW][2][HEADS], [2][HEADS], [8][HEADS]
+    static constexpr int BYTES = 1024 + ML_OFF + (NW * 2 + 10) * HEADS * 4;
     static constexpr bool QREG = NT * D <= 256;                        // q fragments kept in registers
 };
 
 // Joins the warps' and the CTAs' shares and writes the output.  o: float [NW][HEADS][OROW] shares of
-// the CTA's warps, ml: float [NW][2][HEADS] their maxima and sums, then [2][HEADS] for the CTA's own.
+// the CTA's warps; ml: float [NW][2][HEADS] their maxima and sums, then [2][HEADS] for the CTA's own
+// and [8][HEADS] for the weights of the cluster's CTAs.
 template <typename T, int D, int HEADS, int OROW, int NW>
 __device__ __forceinline__ void join_shares(const SparseArgs &a, float *o, float *ml, int ncol, size_t out0, int rank,
                                             int ncta) {
+    constexpr int Q4 = D / 4;  // vectors of four per head
     const int tid = threadIdx.x, nt = NW * 32;
-    float *mine = ml + NW * 2 * HEADS;
+    const float kNegInf = __int_as_float(0xff800000);
+    float *mine = ml + NW * 2 * HEADS, *fr = mine + 2 * HEADS;
     __syncthreads();
     if (tid < HEADS) {
-        float M = __int_as_float(0xff800000), l = 0.f;
+        float M = kNegInf, l = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * 2 * HEADS + tid]);
-        const float Mu = M == __int_as_float(0xff800000) ? 0.f : M;
+        const float Mu = M == kNegInf ? 0.f : M;
+        float f[NW];
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float f = fast_exp2(ml[w * 2 * HEADS + tid] - Mu);
-            l += f * ml[w * 2 * HEADS + HEADS + tid];
-            ml[w * 2 * HEADS + tid] = f;
+            f[w] = fast_exp2(ml[w * 2 * HEADS + tid] - Mu);
+            l += f[w] * ml[w * 2 * HEADS + HEADS + tid];
         }
+        // one CTA: the weights are final
+        const float inv = ncta > 1 ? 1.f : l == 0.f ? 0.f : __fdividef(1.f, l);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) ml[w * 2 * HEADS + tid] = f[w] * inv;
         mine[tid] = M;
         mine[HEADS + tid] = l;
     }
     __syncthreads();
-    if (ncta == 1) {
-        for (int i = tid; i < ncol * (D / 2); i += nt) {
-            const int g = i / (D / 2), d = i % (D / 2) * 2;
-            float x = 0.f, y = 0.f;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) {
-                const float f = ml[w * 2 * HEADS + g];
-                const float2 v = *reinterpret_cast<const float2 *>(o + (w * HEADS + g) * OROW + d);
-                x += f * v.x;
-                y += f * v.y;
-            }
-            const float l = mine[HEADS + g], inv = l == 0.f ? 0.f : __fdividef(1.f, l);
-            store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, x * inv, y * inv);
-        }
-        return;
-    }
-    for (int i = tid; i < ncol * (D / 2); i += nt) {
-        const int g = i / (D / 2), d = i % (D / 2) * 2;
-        float2 s = make_float2(0.f, 0.f);
+    for (int i = tid; i < ncol * Q4; i += nt) {
+        const int g = i / Q4, d = i % Q4 * 4;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             const float f = ml[w * 2 * HEADS + g];
-            const float2 v = *reinterpret_cast<const float2 *>(o + (w * HEADS + g) * OROW + d);
+            const float4 v = *reinterpret_cast<const float4 *>(o + (w * HEADS + g) * OROW + d);
             s.x += f * v.x;
             s.y += f * v.y;
+            s.z += f * v.z;
+            s.w += f * v.w;
         }
-        *reinterpret_cast<float2 *>(o + g * OROW + d) = s;
+        if (ncta == 1) {
+            store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, s.x, s.y);
+            store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d + 2, s.z, s.w);
+        } else {
+            *reinterpret_cast<float4 *>(o + g * OROW + d) = s;
+        }
     }
+    if (ncta == 1) return;
     cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
     cl.sync();
-    // CTA `rank` writes the pairs rank, rank + ncta, ... of the row's output
-    for (int i = rank * nt + tid; i < ncol * (D / 2); i += ncta * nt) {
-        const int g = i / (D / 2), d = i % (D / 2) * 2;
-        float M = __int_as_float(0xff800000), l = 0.f, x = 0.f, y = 0.f;
-        for (int r = 0; r < ncta; ++r) M = fmaxf(M, *cl.map_shared_rank(mine + g, r));
-        if (M == __int_as_float(0xff800000)) M = 0.f;
-        for (int r = 0; r < ncta; ++r) {
-            const float f = fast_exp2(*cl.map_shared_rank(mine + g, r) - M);
-            l += f * *cl.map_shared_rank(mine + HEADS + g, r);
-            const float2 v = *cl.map_shared_rank(reinterpret_cast<float2 *>(o + g * OROW + d), r);
-            x += f * v.x;
-            y += f * v.y;
+    if (tid < HEADS) {
+        float m[8], l[8], M = kNegInf, sum = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            m[r] = r < ncta ? *cl.map_shared_rank(mine + tid, r) : kNegInf;
+            l[r] = r < ncta ? *cl.map_shared_rank(mine + HEADS + tid, r) : 0.f;
+            M = fmaxf(M, m[r]);
         }
-        const float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
-        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, x * inv, y * inv);
+        if (M == kNegInf) M = 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            m[r] = fast_exp2(m[r] - M);
+            sum += m[r] * l[r];
+        }
+        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) fr[r * HEADS + tid] = m[r] * inv;
+    }
+    __syncthreads();
+    // the CTAs take turns at the row's vectors
+    for (int i = rank * nt + tid; i < ncol * Q4; i += ncta * nt) {
+        const int g = i / Q4, d = i % Q4 * 4;
+        float4 v[8], s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < ncta) v[r] = *cl.map_shared_rank(reinterpret_cast<float4 *>(o + g * OROW + d), r);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r < ncta) {
+                const float f = fr[r * HEADS + g];
+                s.x += f * v[r].x;
+                s.y += f * v[r].y;
+                s.z += f * v[r].z;
+                s.w += f * v[r].w;
+            }
+        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, s.x, s.y);
+        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d + 2, s.z, s.w);
     }
     cl.sync();  // no CTA ends while another reads its shares
 }
 
-// The chosen blocks [n_sel] of row r and KV head h, 8 * NT query heads from 8 * NT * grp on.
-// smem: 1024-byte aligned, AttendCfg bytes.  Called by NW * 32 threads of each CTA.
+// The barriers of the warps' rings; before attend_row, and before the previous kernel is waited for.
+template <typename C>
+__device__ __forceinline__ void attend_init(unsigned char *smem) {
+    if (threadIdx.x < C::NW * C::S) mbar_init(reinterpret_cast<uint64_t *>(smem + C::BAR_OFF) + threadIdx.x, 1);
+    fence_mbar_init();
+    __syncthreads();
+}
+
+// The chosen blocks of row r and KV head h, 8 * NT query heads from 8 * NT * grp on.
+// smem: 1024-byte aligned, AttendCfg bytes, after attend_init.  Called by NW * 32 threads of each CTA.
 template <typename T, typename TKV, int D, int NT>
 __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CUtensorMap *tmV, int r, int h, int grp,
                            int rank, int ncta, unsigned char *smem) {
     using C = AttendCfg<T, TKV, D, NT>;
-    constexpr int NW = C::NW, S = C::S, KS = D / 16, MT = D / 16;
+    constexpr int NW = C::NW, S = C::S, NB = C::NB, KS = D / 16, MT = D / 16;
     constexpr bool SPLIT_P = !std::is_same<T, __half>::value;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t sb = smem_addr(smem);
@@ -161,37 +194,61 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
     float *scs = reinterpret_cast<float *>(smem + C::SC_OFF) + warp * S * 2;
     const uint32_t ring = sb + warp * S * C::STAGE;
 
+    // The first copies wait for a chain of loads: list entry, its table entry.  Neither asks
+    // for the row's length or the list's (any entry inside the table is read, and judged
+    // later), so those and q are on their way at the same time.
+    const size_t list = (size_t)r * a.H + h;
+    const int32_t *sel = a.sel + list * a.K, *table = a.tables + (size_t)(r / a.Q) * a.M;
+    const int W = ncta * NW, w = rank * NW + warp;
+    // the warp's blocks: lane l of a batch of 32 holds the l-th
+    int p_j = -1, p_x = -1, p_y = -1;
+    float p_ks = 0.f, p_vs = 0.f;
+    auto load_list = [&](int k) {  // items k .. k + 31
+        const int64_t i = (int64_t)(k + lane) * W + w;
+        p_j = i < a.K ? __ldcg(sel + i) : -1;
+        p_x = p_j >= 0 && p_j < a.M ? __ldcg(table + p_j) : -1;
+    };
+    load_list(0);
+    const int ncol = min(C::HEADS, a.G - grp * C::HEADS);
+    const size_t row0 = ((size_t)r * a.Hq + (size_t)h * a.G + (size_t)grp * C::HEADS) * D;
+    constexpr int QV = C::HEADS * D / 8 / (NW * 32);  // 16-byte vectors of q per thread
+    static_assert(QV * NW * 32 * 8 == C::HEADS * D || (QV == 0 && C::HEADS * D / 8 <= NW * 32), "q vectors");
+    constexpr int QN = QV ? QV : 1;
+    uint4 qv[QN];
+    const bool qvec = ((uintptr_t)a.q & 15) == 0;
+    if (qvec) {
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int e = tid + i * NW * 32;
+            qv[i] = e < ncol * (D / 8) ? __ldg(reinterpret_cast<const uint4 *>(reinterpret_cast<const T *>(a.q) + row0) + e)
+                                       : make_uint4(0, 0, 0, 0);
+        }
+    }
     int b;
     const int L = sparse_row_len(a, r, b), nb = (L + kBlockSize - 1) / kBlockSize;
-    const size_t list = (size_t)r * a.H + h;
     const int n = min(max(__ldcg(a.nsel + list), 0), a.K);
-    const int32_t *sel = a.sel + list * a.K, *table = a.tables + (size_t)b * a.M;
-    const int W = ncta * NW, w = rank * NW + warp, cnt = n > w ? (n - w + W - 1) / W : 0;
+    const int cnt = n > w ? (n - w + W - 1) / W : 0;
 
-    // ---- the warp's blocks: lane l of a batch of 32 holds the l-th ----
-    int p_j = 0, p_y = -1;
-    float p_ks = 0.f, p_vs = 0.f;
-    auto batch = [&](int k) {  // items k .. k + 31
+    auto judge = [&](int k) {
         p_y = -1;
-        if (k + lane < cnt) {
-            p_j = __ldcg(sel + (size_t)(k + lane) * W + w);
-            if (p_j >= 0 && p_j < nb) {  // entries outside the row's blocks are skipped
-                const int x = table[p_j];
-                if (x >= 0 && (int64_t)x < a.N) {
-                    p_y = x * a.H + h;  // host: num_blocks * H below 2^31
-                    if constexpr (C::I8) {
-                        p_ks = a.ks[p_y];
-                        p_vs = a.vs[p_y];
-                    }
-                } else {
-                    raise_flag(PA_EFLAG_BAD_BLOCK);
+        if (k + lane < cnt && p_j >= 0 && p_j < nb) {  // entries outside the row's blocks are skipped
+            if (p_x >= 0 && (int64_t)p_x < a.N) {
+                p_y = p_x * a.H + h;  // host: num_blocks * H below 2^31
+                if constexpr (C::I8) {
+                    p_ks = __ldg(a.ks + p_y);
+                    p_vs = __ldg(a.vs + p_y);
                 }
+            } else {
+                raise_flag(PA_EFLAG_BAD_BLOCK);
             }
         }
     };
     auto issue = [&](int k) {
         if (k >= cnt) return;
-        if (k % 32 == 0) batch(k);
+        if (k % 32 == 0) {
+            if (k > 0) load_list(k);
+            judge(k);
+        }
         const int y = __shfl_sync(0xffffffffu, p_y, k % 32), j = __shfl_sync(0xffffffffu, p_j, k % 32);
         float ks = 0.f, vs = 0.f;
         if constexpr (C::I8) {
@@ -200,11 +257,6 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
         }
         if (lane == 0) {
             const int s = k % S;
-            info[s] = y >= 0 ? min(kBlockSize, L - j * kBlockSize) : 0;
-            if constexpr (C::I8) {
-                scs[2 * s] = ks;
-                scs[2 * s + 1] = vs;
-            }
             if (y >= 0) {
                 mbar_arrive_expect_tx(&bars[s], C::STAGE);
                 tma_tile(ring + s * C::STAGE, tmK, y, smem_addr(&bars[s]));
@@ -212,21 +264,26 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
             } else {
                 mbar_arrive(&bars[s]);
             }
+            info[s] = y >= 0 ? min(kBlockSize, L - j * kBlockSize) : 0;
+            if constexpr (C::I8) {
+                scs[2 * s] = ks;
+                scs[2 * s + 1] = vs;
+            }
         }
         __syncwarp();
     };
-    if (lane == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
-        fence_mbar_init();
-    }
-    __syncwarp();
 #pragma unroll
     for (int k = 0; k < S; ++k) issue(k);
 
     // ---- q: rows of 8 * NT heads, zeros past the group ----
-    const int ncol = min(C::HEADS, a.G - grp * C::HEADS);
-    const size_t row0 = ((size_t)r * a.Hq + (size_t)h * a.G + (size_t)grp * C::HEADS) * D;
-    {
+    if (qvec) {
+#pragma unroll
+        for (int i = 0; i < QN; ++i) {
+            const int e = tid + i * NW * 32;
+            if (e < C::HEADS * (D / 8))
+                *reinterpret_cast<uint4 *>(smem + C::Q_OFF + (e / (D / 8)) * C::QROW + (e % (D / 8)) * 16) = qv[i];
+        }
+    } else {
         uint16_t *qd = reinterpret_cast<uint16_t *>(smem + C::Q_OFF);
         const uint16_t *qsrc = reinterpret_cast<const uint16_t *>(a.q) + row0;
         for (int i = tid; i < C::HEADS * D; i += NW * 32) {
@@ -235,27 +292,26 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
         }
     }
     __syncthreads();
-    // B fragment of k-step ks, n-tile nt: the dims in the order of the K fragments
-    auto qfrag = [&](int nt, int ks, uint32_t &b0, uint32_t &b1) {
-        const uint32_t row = sb + C::Q_OFF + (nt * 8 + g) * C::QROW;
+    // B fragments of k-steps ks (and, 16-bit caches, ks + 1) of n-tile t, the dims in the order of
+    // the K fragments
+    auto qfrag = [&](int t, int ks, uint32_t (&f)[4]) {
         if constexpr (!C::I8) {
-            b0 = lds_u32(row + (ks * 16 + 2 * c) * 2);
-            b1 = lds_u32(row + (ks * 16 + 2 * c + 8) * 2);
+            ldsm_x4(f, sb + C::Q_OFF + (t * 8 + (lane & 7)) * C::QROW + ks * 32 + (lane >> 3) * 16);
         } else {
             // thread column c reads 32 (D = 64: 16) contiguous bytes per 128-byte segment of a row
             const int d0 = D == 64 ? c * 16 + ks * 4 : (ks / 8) * 128 + c * 32 + (ks % 8) * 4;
-            uint32_t v[2];
-            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(row + d0 * 2) : "memory");
-            b0 = v[0];
-            b1 = v[1];
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                         : "r"(sb + C::Q_OFF + (t * 8 + g) * C::QROW + d0 * 2)
+                         : "memory");
         }
     };
-    uint32_t qb[C::QREG ? NT : 1][C::QREG ? KS : 1][2];
+    uint32_t qb[C::QREG ? NT : 1][C::QREG ? KS / 2 : 1][4];
     if constexpr (C::QREG) {
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) qfrag(t, ks, qb[t][ks][0], qb[t][ks][1]);
+            for (int ks = 0; ks < KS; ks += 2) qfrag(t, ks, qb[t][ks / 2]);
     }
 
     float o[NT][MT][4] = {};
@@ -266,157 +322,203 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
         l[t][0] = l[t][1] = 0.f;
     }
 
-    for (int k = 0; k < cnt; ++k) {
-        const int s = k % S;
-        // (the lanes give up together)
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[s], (k / S) & 1, a.wait_ns))) {
-            // give up: the copies still in flight are waited for (again with a limit), so that
-            // none lands in memory that the joining reuses
-            for (int i = 1; i < S && k + i < cnt; ++i) mbar_wait(&bars[(k + i) % S], ((k + i) / S) & 1, a.wait_ns);
+    for (int k = 0; k < cnt; k += NB) {
+        bool landed = true;
+#pragma unroll
+        for (int n1 = 0; n1 < NB; ++n1)
+            if (k + n1 < cnt) landed &= mbar_wait(&bars[(k + n1) % S], ((k + n1) / S) & 1, a.wait_ns);
+        if (!__all_sync(0xffffffffu, landed)) {  // (the lanes give up together)
+            // the copies still in flight are waited for, again with a limit, so that none lands
+            // in memory that the joining reuses
+            for (int i = NB; i < S && k + i < cnt; ++i) mbar_wait(&bars[(k + i) % S], ((k + i) / S) & 1, a.wait_ns);
             break;
         }
-        __syncwarp();
-        const int valid = info[s];
-        const uint32_t kt = ring + s * C::STAGE, vt = kt + C::TILE;
-        if (valid > 0) {
-            // ---- S^T ----
-            float x[NT][4];
-            {
-                float acc[2][NT][4];
+        int valid[NB];
+        uint32_t kt[NB], vt[NB];
+        bool whole = true;
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+        for (int n1 = 0; n1 < NB; ++n1) {
+            const int s = (k + n1) % S;
+            valid[n1] = k + n1 < cnt ? info[s] : 0;
+            whole &= valid[n1] == kBlockSize;
+            kt[n1] = ring + s * C::STAGE;
+            vt[n1] = kt[n1] + C::TILE;
+        }
+        // ---- S^T ----
+        float x[NB][NT][4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[0][t][e] = acc[1][t][e] = 0.f;
+        for (int n1 = 0; n1 < NB; ++n1)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n1][t][e] = 0.f;
+#pragma unroll
+        for (int k2 = 0; k2 < KS; k2 += 2) {
+            uint32_t qf[C::QREG ? 1 : NT][4];
+            if constexpr (!C::QREG) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) qfrag(t, k2, qf[t]);
+            }
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+                uint32_t af[2][4];
                 if constexpr (!C::I8) {
                     const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
 #pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        uint32_t af[4];
-                        const int ch = ks * 2 + (lane >> 4);
-                        ldsm_x4(af, swz(kt + (ch >> 3) * 2048, row, ch & 7));
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            uint32_t b0, b1;
-                            if constexpr (C::QREG) {
-                                b0 = qb[t][ks][0];
-                                b1 = qb[t][ks][1];
-                            } else {
-                                qfrag(t, ks, b0, b1);
-                            }
-                            Mma<T>::mma(acc[ks & 1][t], af, b0, b1);
-                        }
+                    for (int u = 0; u < 2; ++u) {
+                        const int ch = (k2 + u) * 2 + (lane >> 4);
+                        ldsm_x4(af[u], swz(kt[n1] + (ch >> 3) * 2048, row, ch & 7));
                     }
                 } else {
-                    constexpr int V = D == 64 ? 1 : 2;  // 16-byte vectors per thread and segment
+                    // 8 bytes of tokens g and g + 8
+                    uint32_t wa[2], wb[2];
+                    uint32_t pa, pb;
+                    if constexpr (D == 64) {
+                        pa = kt[n1] + g * 64 + c * 16 + k2 * 4;
+                        pb = pa + 8 * 64;
+                    } else {
+                        const uint32_t seg = kt[n1] + (k2 / 8) * 2048;
+                        pa = swz(seg, g, 2 * c + (k2 % 8) / 4) + (k2 % 4) * 4;
+                        pb = swz(seg, g + 8, 2 * c + (k2 % 8) / 4) + (k2 % 4) * 4;
+                    }
+                    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(wa[0]), "=r"(wa[1]) : "r"(pa) : "memory");
+                    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(wb[0]), "=r"(wb[1]) : "r"(pb) : "memory");
 #pragma unroll
-                    for (int sg = 0; sg < (D == 64 ? 1 : D / 128); ++sg) {
-#pragma unroll
-                        for (int v = 0; v < V; ++v) {
-                            uint32_t wa[4], wb[4];
-                            if constexpr (D == 64) {
-                                lds_v4(wa, kt + g * 64 + c * 16);
-                                lds_v4(wb, kt + (g + 8) * 64 + c * 16);
-                            } else {
-                                lds_v4(wa, swz(kt + sg * 2048, g, 2 * c + v));
-                                lds_v4(wb, swz(kt + sg * 2048, g + 8, 2 * c + v));
-                            }
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const int ks = sg * 8 + v * 4 + u;
-                                const uint32_t ua = wa[u] ^ 0x80808080u, ub = wb[u] ^ 0x80808080u;
-                                const uint32_t af[4] = {i8_pair<T>(ua, 0, 1), i8_pair<T>(ub, 0, 1), i8_pair<T>(ua, 2, 3),
-                                                        i8_pair<T>(ub, 2, 3)};
-#pragma unroll
-                                for (int t = 0; t < NT; ++t) {
-                                    uint32_t b0, b1;
-                                    if constexpr (C::QREG) {
-                                        b0 = qb[t][ks][0];
-                                        b1 = qb[t][ks][1];
-                                    } else {
-                                        qfrag(t, ks, b0, b1);
-                                    }
-                                    Mma<T>::mma(acc[ks & 1][t], af, b0, b1);
-                                }
-                            }
-                        }
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t ua = wa[u] ^ 0x80808080u, ub = wb[u] ^ 0x80808080u;
+                        af[u][0] = i8_pair<T>(ua, 0, 1);
+                        af[u][1] = i8_pair<T>(ub, 0, 1);
+                        af[u][2] = i8_pair<T>(ua, 2, 3);
+                        af[u][3] = i8_pair<T>(ub, 2, 3);
                     }
                 }
-                const float sc = C::I8 ? a.scale_log2 * scs[2 * s] : a.scale_log2;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint32_t *f = C::QREG ? qb[t][k2 / 2] : qf[t];
+                        Mma<T>::mma(x[n1][t], af[u], f[2 * u], f[2 * u + 1]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int n1 = 0; n1 < NB; ++n1) {
+            const float sc = C::I8 ? a.scale_log2 * scs[2 * ((k + n1) % S)] : a.scale_log2;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n1][t][e] *= sc;
+        }
+        if (!whole) {  // rows past the last token hold anything, NaN among it
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // rows past the last token hold anything, NaN among it
-                        const bool in = g + 8 * (e >> 1) < valid;
-                        x[t][e] = in ? (acc[0][t][e] + acc[1][t][e]) * sc : __int_as_float(0xff800000);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (g + 8 * (e >> 1) >= valid[n1]) x[n1][t][e] = __int_as_float(0xff800000);
+        }
+        // ---- running maximum and sum; P ----
+        // The reference of the exponentials follows the maximum only when that grew by more than
+        // 2^8: weights of up to 2^8 are as exact, and the output is seldom rescaled.
+        uint32_t ph[NB][NT][2], pl[SPLIT_P ? NB : 1][SPLIT_P ? NT : 1][2];
+        float mx[NT][2];
+        bool grew = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = fmaxf(x[0][t][e], x[0][t][2 + e]);
+                if constexpr (NB > 1) v = fmaxf(v, fmaxf(x[1][t][e], x[1][t][2 + e]));
+                mx[t][e] = v;
             }
-            // ---- running maximum and sum; P ----
-            uint32_t ph[NT][2], pl[NT][2];
-            bool moved = false;
-            float al[NT][2];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mx[t][e] = fmaxf(mx[t][e], __shfl_xor_sync(0xffffffffu, mx[t][e], d));
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) grew |= mx[t][e] > m[t][e] + 8.f;
+        if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
+                float al[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(x[t][e], x[t][2 + e]);
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    const float mn = fmaxf(m[t][e], mx);
-                    const float mu = mn == __int_as_float(0xff800000) ? 0.f : mn;
-                    al[t][e] = fast_exp2(m[t][e] - mu);
-                    moved |= mn != m[t][e];
+                    const float mn = mx[t][e] > m[t][e] + 8.f ? mx[t][e] : m[t][e];
+                    al[e] = m[t][e] == mn ? 1.f : fast_exp2(m[t][e] - mn);
                     m[t][e] = mn;
-                    x[t][e] = fast_exp2(x[t][e] - mu);
-                    x[t][2 + e] = fast_exp2(x[t][2 + e] - mu);
-                    l[t][e] = l[t][e] * al[t][e] + (x[t][e] + x[t][2 + e]);
+                    l[t][e] *= al[e];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][i][e] *= al[e & 1];
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float mu[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mu[e] = m[t][e] == __int_as_float(0xff800000) ? 0.f : m[t][e];
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[n1][t][e] = fast_exp2(x[n1][t][e] - mu[e & 1]);
+                    l[t][e & 1] += x[n1][t][e];
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {  // tokens g (e = 0) and g + 8, heads 2c, 2c + 1
-                    const uint32_t hi = Mma<T>::pack(x[t][2 * e], x[t][2 * e + 1]);
-                    ph[t][e] = movm_t(hi);
+                    const uint32_t hi = Mma<T>::pack(x[n1][t][2 * e], x[n1][t][2 * e + 1]);
+                    ph[n1][t][e] = movm_t(hi);
                     if constexpr (SPLIT_P) {
                         const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
-                        pl[t][e] = movm_t(Mma<T>::pack(x[t][2 * e] - h0, x[t][2 * e + 1] - h1));
+                        pl[n1][t][e] = movm_t(Mma<T>::pack(x[n1][t][2 * e] - h0, x[n1][t][2 * e + 1] - h1));
                     }
                 }
             }
-            if (__any_sync(0xffffffffu, moved)) {
+        }
+        // ---- O^T ----
+        if constexpr (!C::I8) {
+            if (!whole) {
+                // values behind the last token: a weight of 0 does not make a NaN there 0
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[t][i][e] *= al[t][e & 1];
-            }
-            // ---- O^T ----
-            if constexpr (!C::I8) {
-                if (valid < kBlockSize) {
-                    // values behind the last token: a weight of 0 does not make a NaN there 0
-                    for (int i = lane; i < (kBlockSize - valid) * (C::ROWB / 16); i += 32) {
-                        const int row = valid + i / (C::ROWB / 16), ch = i % (C::ROWB / 16);
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(swz(vt + (ch >> 3) * 2048, row, ch & 7)),
+                for (int n1 = 0; n1 < NB; ++n1)
+                    for (int i = lane; i < (kBlockSize - valid[n1]) * (C::ROWB / 16); i += 32) {
+                        const int row = valid[n1] + i / (C::ROWB / 16), ch = i % (C::ROWB / 16);
+                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                         swz(vt[n1] + (ch >> 3) * 2048, row, ch & 7)),
                                      "r"(0)
                                      : "memory");
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                const int row = (lane & 7) + ((lane >> 4) & 1) * 8;
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            const int row = (lane & 7) + ((lane >> 4) & 1) * 8;
 #pragma unroll
-                for (int i = 0; i < MT; ++i) {
+            for (int i = 0; i < MT; ++i) {
+                const int ch = i * 2 + ((lane >> 3) & 1);
+#pragma unroll
+                for (int n1 = 0; n1 < NB; ++n1) {
                     uint32_t af[4];
-                    const int ch = i * 2 + ((lane >> 3) & 1);
-                    ldsm_x4_t(af, swz(vt + (ch >> 3) * 2048, row, ch & 7));
+                    ldsm_x4_t(af, swz(vt[n1] + (ch >> 3) * 2048, row, ch & 7));
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
-                        Mma<T>::mma(o[t][i], af, ph[t][0], ph[t][1]);
-                        if constexpr (SPLIT_P) Mma<T>::mma(o[t][i], af, pl[t][0], pl[t][1]);
+                        Mma<T>::mma(o[t][i], af, ph[n1][t][0], ph[n1][t][1]);
+                        if constexpr (SPLIT_P) Mma<T>::mma(o[t][i], af, pl[n1][t][0], pl[n1][t][1]);
                     }
                 }
-            } else {
-                const float vs = scs[2 * s + 1];
-                constexpr int MS = D == 64 ? 4 : 8, VW = D == 64 ? 2 : 4;  // m-tiles and words per segment
+            }
+        } else {
+            constexpr int MS = D == 64 ? 4 : 8, VW = D == 64 ? 2 : 4;  // m-tiles and words per segment
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+                // a block that is not there: its codes are whatever the stage held, times 0
+                const float vs = valid[n1] > 0 ? scs[2 * ((k + n1) % S) + 1] : 0.f;
 #pragma unroll
                 for (int sg = 0; sg < MT / MS; ++sg) {
                     uint32_t rw[4][4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
@@ -426,10 +528,10 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
                         if constexpr (D == 64) {
                             asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
                                          : "=r"(rw[q][0]), "=r"(rw[q][1])
-                                         : "r"(vt + row * 64 + g * 8)
+                                         : "r"(vt[n1] + row * 64 + g * 8)
                                          : "memory");
                         } else {
-                            lds_v4(rw[q], swz(vt + sg * 2048, row, g));
+                            lds_v4(rw[q], swz(vt[n1] + sg * 2048, row, g));
                         }
 #pragma unroll
                         for (int e = 0; e < VW; ++e) rw[q][e] ^= 0x80808080u;
@@ -446,8 +548,8 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
                             float d[4];
-                            Mma<T>::mma0(d, af, ph[t][0], ph[t][1]);
-                            if constexpr (SPLIT_P) Mma<T>::mma(d, af, pl[t][0], pl[t][1]);
+                            Mma<T>::mma0(d, af, ph[n1][t][0], ph[n1][t][1]);
+                            if constexpr (SPLIT_P) Mma<T>::mma(d, af, pl[n1][t][0], pl[n1][t][1]);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) o[t][sg * MS + i][e] += vs * d[e];
                         }
@@ -456,7 +558,8 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
             }
         }
         __syncwarp();
-        issue(k + S);
+#pragma unroll
+        for (int n1 = 0; n1 < NB; ++n1) issue(k + S + n1);
     }
 
     // ---- this warp's share, then the joining ----
@@ -500,7 +603,7 @@ struct AttendF32Cfg {
     static constexpr int NW = 4, OROW = D + 4;
     static constexpr int Q_OFF = NW * GT * OROW * 4;
     static constexpr int ML_OFF = Q_OFF + GT * D * 4;
-    static constexpr int BYTES = ML_OFF + (NW + 1) * 2 * GT * 4;
+    static constexpr int BYTES = ML_OFF + (NW * 2 + 10) * GT * 4;
 };
 
 template <int D, int GT>

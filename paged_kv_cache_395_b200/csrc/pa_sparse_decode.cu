@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(128) attend_kernel(const __grid_constant__ CUt
         prefetch_tensormap(&tmK);
         prefetch_tensormap(&tmV);
     }
+    attend_init<AttendCfg<T, TKV, D, NT>>(smem);
     pdl_wait();
     pdl_release_dependents();
     cg::cluster_group cl = cg::this_cluster();
