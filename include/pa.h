@@ -454,7 +454,9 @@ int pa_quantize_int4(const void *src_cache, int src_dtype, uint8_t *dst_cache, f
  * or its last, partly filled block has a refcount above one (PA_EFLAG_BAD_LENGTH; copy
  * that block first, see pa_block_copy), or when that block's table entry is outside the
  * pool (PA_EFLAG_BAD_BLOCK).  Entries of finished rows outside the pool are not pushed
- * (PA_EFLAG_BAD_BLOCK).
+ * (PA_EFLAG_BAD_BLOCK).  An entry outside the pool that is popped off the list is handed out
+ * with PA_EFLAG_BAD_BLOCK: slots in it are -1, and the sequence's other slots and positions
+ * may be.  Without refcounts a block belongs to one sequence.
  *
  * seq_lens_out may be seq_lens, and free_count_out free_count; otherwise the buffers do
  * not overlap.  refcounts [num_blocks], positions [max_tokens] and row_starts may be NULL.

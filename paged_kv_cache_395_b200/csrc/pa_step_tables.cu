@@ -11,11 +11,13 @@
 // dependent loads (lengths -> last block's table entry -> stack entries -> stores), not by
 // bytes: one step of 64 sequences moves under 5 KB.
 //
-// One thread-block cluster, so that a step is one launch: every CTA computes the prefix
-// sums over all sequences for itself (8 bytes of input per sequence), and the CTAs share
-// the blocks given back, the blocks handed out and the token slots.  Blocks are pushed
-// before they are popped; the cluster's barrier, which also makes the pushes visible,
-// stands between the two.
+// One thread-block cluster: every CTA computes the prefix sums over all sequences for
+// itself (8 bytes of input per sequence), and the CTAs share the blocks given back and
+// handed out.  Blocks are pushed before they are popped; the cluster's barrier, which also
+// makes the pushes visible, stands between the two.  The slots of a step with few tokens are
+// written by the same launch.  A step with prompts has so many that a cluster's few SMs
+// would be the bound (526k slots: 85 us), so a second kernel writes them over the whole GPU,
+// from the tables and lengths that the first one left.
 #include <cooperative_groups.h>
 
 #include <atomic>
@@ -33,7 +35,7 @@ namespace {
 
 constexpr int kClaim = 1 << 30;  // refs[x] = kClaim + e: entry e is the last one of this call that freed x
 
-// Inclusive prefix sum of one value per thread over the CTA (ws: one slot per warp).
+// Inclusive prefix sum of one value per thread over the CTA (ws: 32 slots); total: of all threads.
 template <typename V>
 __device__ __forceinline__ V block_scan(V x, V *ws, V *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -44,15 +46,16 @@ __device__ __forceinline__ V block_scan(V x, V *ws, V *total) {
     }
     if (lane == 31) ws[warp] = x;
     __syncthreads();
-    V before = 0, all = 0;
-    for (int w = 0; w < nw; ++w) {
-        const V s = ws[w];
-        if (w < warp) before += s;
-        all += s;
+    V s = lane < nw ? ws[lane] : 0;  // every warp scans the warps' sums
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const V y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
     }
+    *total = __shfl_sync(0xffffffffu, s, 31);
+    const V before = __shfl_sync(0xffffffffu, s, (warp + 31) & 31);
     __syncthreads();
-    *total = all;
-    return x + before;
+    return warp ? x + before : x;
 }
 
 // Largest b in [lo, B) with start[b] <= t, where start is non-decreasing and start[lo] <= t: doubling
@@ -70,64 +73,76 @@ __device__ __forceinline__ int row_of(const int *start, int lo, int B, int t) {
 
 __device__ __forceinline__ int blocks_of(int tokens) { return (int)(((unsigned)tokens + kBlockSize - 1) / kBlockSize); }
 
-// Shared memory: per sequence, the exclusive prefix sums (B + 1 entries), the length, the
-// table entry of the last, partly filled block (-1: none) and whether it is served.
+// Shared memory: per sequence, the exclusive prefix sums (B + 1 entries), the length, the new
+// tokens, the table entry of the last, partly filled block (-1: none) and whether it is served.
 struct Smem {
-    int *tok, *rel, *need, *len, *last;
+    int *tok, *rel, *need, *len, *add, *last;
     uint8_t *ok;
     __device__ Smem(unsigned char *p, int B) {
         tok = reinterpret_cast<int *>(p);
         rel = tok + B + 1;
         need = rel + B + 1;
         len = need + B + 1;
-        last = len + B;
+        add = len + B;
+        last = add + B;
         ok = reinterpret_cast<uint8_t *>(last + B);
     }
-    static size_t bytes(int B) { return (size_t)(3 * (B + 1) + 2 * B) * 4 + B + 16; }
+    static size_t bytes(int B) { return (size_t)(3 * (B + 1) + 3 * B) * 4 + B + 16; }
 };
 
+// WRITE_SLOTS: this launch also writes the slots and positions; otherwise it only leaves the slot
+// of each sequence's first token, -1 if it is not served, for step_slots_kernel.
+template <bool WRITE_SLOTS>
 __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ long long ws64[32];
     __shared__ int ws32[32];
-    __shared__ int s_kept;  // blocks this CTA pushes
+    __shared__ int s_kept, s_claim;  // blocks this CTA pushes; whether it met one that several entries freed
     const Smem s(smem_raw, a.B);
     const int tid = threadIdx.x, nt = blockDim.x, B = a.B, M = a.M, N = a.N, T = a.T;
     cg::cluster_group cl = cg::this_cluster();
     const int rank = (int)cl.block_rank(), ncta = (int)cl.num_blocks();
     const int top = M * kBlockSize;  // host: M <= 2^26
+    auto barrier = [&]() {  // of the cluster; its writes are visible after it
+        if (ncta > 1)
+            cl.sync();
+        else
+            __syncthreads();
+    };
 
     pdl_wait();
     pdl_release_dependents();
 
-    int count = a.count[0];
-    if (count < 0 || count > N) {
-        if (tid == 0 && rank == 0) raise_flag(PA_EFLAG_FREE_LIST);
-        count = count < 0 ? 0 : N;
-    }
-
     // ---- lengths, and the prefix sums of new tokens and of blocks given back ----
+    int count = __ldcg(a.count);
     const int per = (B + nt - 1) / nt, b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long tok = 0, tok_all;
     int rel = 0, rel_all;
     for (int b = b0; b < b1; ++b) {
-        const int L = a.lens[b], n = a.news[b];
-        s.len[b] = L;
+        const int L = __ldcg(a.lens + b), n = __ldcg(a.news + b);
         const bool good = L >= 0 && n >= PA_SEQ_FINISHED && (long long)L + max(n, 0) <= top;
+        // the last, partly filled block: asked for now, looked at after the sums
+        s.last[b] = good && n > 0 && L % kBlockSize ? __ldcg(a.tables + (size_t)b * M + L / kBlockSize) : -1;
+        s.len[b] = L;
+        s.add[b] = n;
         if (!good && rank == 0) raise_flag(PA_EFLAG_BAD_LENGTH);
         tok += max(n, 0);
         rel += good && n == PA_SEQ_FINISHED ? blocks_of(L) : 0;
         // 0: nothing to do, 1: to be served, 2: finished
         s.ok[b] = !good ? 0 : n == PA_SEQ_FINISHED ? 2 : n > 0 ? 1 : 0;
     }
+    if (count < 0 || count > N) {
+        if (tid == 0 && rank == 0) raise_flag(PA_EFLAG_FREE_LIST);
+        count = count < 0 ? 0 : N;
+    }
     tok = block_scan(tok, ws64, &tok_all) - tok;
     rel = block_scan(rel, ws32, &rel_all) - rel;
     for (int b = b0; b < b1; ++b) {
-        const int L = s.len[b], n = a.news[b];
+        const int n = s.add[b];
         s.tok[b] = (int)min(tok, (long long)T + 1);
         s.rel[b] = rel;
         tok += max(n, 0);
-        rel += s.ok[b] == 2 ? blocks_of(L) : 0;
+        rel += s.ok[b] == 2 ? blocks_of(s.len[b]) : 0;
         if (n > 0 && tok > T) {  // the sequence's tokens do not fit into the slot buffer
             s.ok[b] = 0;
             if (rank == 0) raise_flag(PA_EFLAG_BAD_LENGTH);
@@ -147,70 +162,118 @@ __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
             return a.tables[(size_t)b * M + (e - s.rel[b])];
         };
         auto inside = [&](int x) { return x >= 0 && x < N; };
+        // a thread's first entries stay in registers (usually they are all)
+        constexpr int E = 4;
+        const int f0 = e0 + tid;
+        int x0[E], old0[E];
+        uint32_t k0 = 0;  // which of them are pushed
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            x0[i] = f0 + i * nt < e1 ? entry(f0 + i * nt) : -1;
+            old0[i] = 0;
+        }
+        bool claim = false;
         if (a.refs) {
-            for (int e = e0 + tid; e < e1; e += nt) {
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                if (inside(x0[i])) old0[i] = atomicSub(a.refs + x0[i], 1);
+            for (int e = f0 + E * nt; e < e1; e += nt) {
                 const int x = entry(e);
-                if (inside(x)) atomicSub(a.refs + x, 1);
+                if (inside(x)) claim |= atomicSub(a.refs + x, 1) > 1;
             }
-            cl.sync();
-            // the last entry of a block whose count reached zero claims it
-            for (int e = e0 + tid; e < e1; e += nt) {
+            barrier();
+        }
+        // A block whose count reached zero is pushed.  If several entries of this call brought it
+        // there (some saw a count above one), the last of them pushes it, which takes another
+        // round, as does a count below zero; without such blocks each entry knows by itself.
+        int kept = 0, all_kept;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if (f0 + i * nt >= e1) continue;
+            if (!inside(x0[i])) {
+                raise_flag(PA_EFLAG_BAD_BLOCK);
+                continue;
+            }
+            const int v = a.refs ? __ldcg(a.refs + x0[i]) : 0;
+            if (v < 0) raise_flag(PA_EFLAG_FREE_LIST);
+            claim |= v < 0 || (v == 0 && old0[i] > 1);
+            kept += v == 0;
+            k0 |= (uint32_t)(v == 0) << i;
+        }
+        for (int e = f0 + E * nt; e < e1; e += nt) {
+            const int x = entry(e);
+            if (!inside(x)) {
+                raise_flag(PA_EFLAG_BAD_BLOCK);
+                continue;
+            }
+            const int v = a.refs ? __ldcg(a.refs + x) : 0;
+            if (v < 0) raise_flag(PA_EFLAG_FREE_LIST);
+            claim |= v < 0;
+            kept += v == 0;
+        }
+        block_scan(kept, ws32, &all_kept);
+        claim = __syncthreads_or(claim);
+        if (tid == 0) {
+            s_kept = all_kept;
+            s_claim = claim;
+        }
+        barrier();
+        for (int r = 0; r < ncta && ncta > 1; ++r) claim |= *cl.map_shared_rank(&s_claim, r) != 0;
+        if (claim) {  // the same in every CTA
+            for (int e = f0; e < e1; e += nt) {
                 const int x = entry(e);
                 if (!inside(x)) continue;
                 const int v = __ldcg(a.refs + x);
                 if (v == 0 || v >= kClaim) atomicMax(a.refs + x, kClaim + e);
             }
-            cl.sync();
+            barrier();
+            kept = 0;
+            k0 = 0;
+            for (int e = f0, i = 0; e < e1; e += nt, ++i) {
+                const int x = entry(e);
+                const bool k = inside(x) && __ldcg(a.refs + x) == kClaim + e;
+                kept += k;
+                if (i < E) k0 |= (uint32_t)k << i;
+            }
+            block_scan(kept, ws32, &all_kept);
+            if (tid == 0) s_kept = all_kept;
+            barrier();
         }
-        auto keep = [&](int e, int x) { return inside(x) && (!a.refs || __ldcg(a.refs + x) == kClaim + e); };
-        int mine = 0;
-        for (int e = e0 + tid; e < e1; e += nt) {
-            const int x = entry(e);
-            mine += keep(e, x);
-            if (!inside(x)) raise_flag(PA_EFLAG_BAD_BLOCK);
-            if (a.refs && inside(x) && __ldcg(a.refs + x) < 0) raise_flag(PA_EFLAG_FREE_LIST);
-        }
-        int kept;
-        block_scan(mine, ws32, &kept);
-        if (tid == 0) s_kept = kept;
-        cl.sync();
         int at = count, pushed = 0;
         for (int r = 0; r < ncta; ++r) {
-            const int k = *cl.map_shared_rank(&s_kept, r);
+            const int k = ncta > 1 ? *cl.map_shared_rank(&s_kept, r) : all_kept;
             if (r < rank) at += k;
             pushed += k;
         }
-        for (int e = e0; e < e1; e += nt) {  // in order, nt entries at a time
-            const int f = e + tid;
-            const int x = f < e1 ? entry(f) : -1;
-            const bool k = f < e1 && keep(f, x);
+        auto push = [&](int x, bool k) {  // the next nt entries, in order
             int all;
             const int nth = at + block_scan((int)k, ws32, &all) - 1;
-            if (k) {
-                if (nth < N) a.free_blocks[nth] = x;
-                if (a.refs) a.refs[x] = 0;
-            } else if (f < e1 && a.refs && inside(x) && __ldcg(a.refs + x) < 0) {
-                a.refs[x] = 0;
-            }
+            if (k && nth < N) a.free_blocks[nth] = x;
+            if (claim && inside(x) && (k || __ldcg(a.refs + x) < 0)) a.refs[x] = 0;
             at += all;
+        };
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            if (e0 + i * nt < e1) push(x0[i], k0 >> i & 1);
+        for (int e = e0 + E * nt; e < e1; e += nt) {
+            const int f = e + tid, x = f < e1 ? entry(f) : -1;
+            push(x, inside(x) && (!a.refs || __ldcg(a.refs + x) == (claim ? kClaim + f : 0)));
         }
         if ((long long)count + pushed > N) {
             if (tid == 0 && rank == 0) raise_flag(PA_EFLAG_FREE_LIST);
             pushed = N - count;
         }
         count += pushed;
-        cl.sync();  // every push is visible before the first pop
+        barrier();  // every push is visible before the first pop
     }
 
     // ---- needs, in order, while the list lasts ----
     int need = 0, need_all;
     for (int b = b0; b < b1; ++b) {
-        s.last[b] = -1;
         if (s.ok[b] != 1) continue;
         const int L = s.len[b];
         if (L % kBlockSize) {
-            const int x = a.tables[(size_t)b * M + L / kBlockSize];
-            s.last[b] = x;
+            const int x = s.last[b];
             const bool in = x >= 0 && x < N;
             if (!in || (a.refs && __ldcg(a.refs + x) > 1)) {
                 s.ok[b] = 0;
@@ -218,14 +281,14 @@ __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
                 continue;
             }
         }
-        need += blocks_of(L + a.news[b]) - blocks_of(L);
+        need += blocks_of(L + s.add[b]) - blocks_of(L);
     }
     need = block_scan(need, ws32, &need_all) - need;
     int served = 0;  // the most blocks handed out up to a served sequence of this thread
     for (int b = b0; b < b1; ++b) {
         s.need[b] = need;
         if (s.ok[b] != 1) continue;
-        const int k = blocks_of(s.len[b] + a.news[b]) - blocks_of(s.len[b]);
+        const int k = blocks_of(s.len[b] + s.add[b]) - blocks_of(s.len[b]);
         need += k;
         if (k > 0 && need > count) {
             s.ok[b] = 0;
@@ -234,45 +297,100 @@ __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
             served = need;
         }
     }
-    if (tid == 0) s.need[B] = need_all;
     // the needs grow along the sequences, so those handed out are a prefix of all needs
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) served = max(served, __shfl_xor_sync(0xffffffffu, served, o));
+    served = __reduce_max_sync(0xffffffffu, served);
     if ((tid & 31) == 0) ws32[tid >> 5] = served;
     __syncthreads();
-    for (int w = 0; w < nt / 32; ++w) served = max(served, ws32[w]);
+    served = __reduce_max_sync(0xffffffffu, (tid & 31) < nt / 32 ? ws32[tid & 31] : 0);
 
     // every CTA has read the lengths, the count and the entries that others write below
     if (ncta > 1) cl.sync();
 
     // ---- results ----
-    if (rank == 0) {
-        for (int b = tid; b < B; b += nt)
-            a.lens_out[b] = s.ok[b] == 2 ? 0 : s.ok[b] == 1 ? s.len[b] + a.news[b] : s.len[b];
-        if (a.starts)
-            for (int b = tid; b <= B; b += nt) a.starts[b] = min(s.tok[b], T);
-        if (tid == 0) a.count_out[0] = count - served;
-    }
     const int gid = rank * nt + tid, gn = ncta * nt;
-    for (int i = gid; i < served; i += gn) {
-        const int b = row_of(s.need, 0, B, i);
-        const int x = __ldcg(a.free_blocks + count - 1 - i);
-        a.tables[(size_t)b * M + blocks_of(s.len[b]) + (i - s.need[b])] = x;
-        if (a.refs && x >= 0 && x < N) a.refs[x] = 1;
-        if (x < 0 || x >= N) raise_flag(PA_EFLAG_BAD_BLOCK);
+    {  // each thread a run of the popped blocks
+        const int q = (served + gn - 1) / gn, i0 = min(served, gid * q), i1 = min(served, i0 + q);
+        int b = i0 < i1 ? row_of(s.need, 0, B, i0) : 0;
+        for (int i = i0; i < i1; i += 4) {
+            int x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = i + e < i1 ? __ldcg(a.free_blocks + count - 1 - i - e) : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (i + e >= i1) break;
+                b = row_of(s.need, b, B, i + e);
+                a.tables[(size_t)b * M + blocks_of(s.len[b]) + (i + e - s.need[b])] = x[e];
+                if (x[e] < 0 || x[e] >= N)
+                    raise_flag(PA_EFLAG_BAD_BLOCK);
+                else if (a.refs)
+                    a.refs[x[e]] = 1;
+            }
+        }
     }
-    const int live = s.tok[B];
+    // slot of token i of served sequence b
+    auto slot_of = [&](int b, int i) {
+        const int p = s.len[b] + i, k = p / kBlockSize - blocks_of(s.len[b]);  // k < 0: in the partly filled block
+        const int x = k < 0 ? s.last[b] : __ldcg(a.free_blocks + count - 1 - s.need[b] - k);
+        return x >= 0 && x < N ? (long long)x * kBlockSize + p % kBlockSize : -1ll;
+    };
+    for (int b = gid; b < B; b += gn) {
+        a.lens_out[b] = s.ok[b] == 2 ? 0 : s.ok[b] == 1 ? s.len[b] + s.add[b] : s.len[b];
+        if (!WRITE_SLOTS && s.add[b] > 0 && s.tok[b] < T) a.slots[s.tok[b]] = s.ok[b] == 1 ? slot_of(b, 0) : -1;
+    }
+    if (a.starts)
+        for (int b = gid; b <= B; b += gn) a.starts[b] = min(s.tok[b], T);
+    if (gid == 0) a.count_out[0] = count - served;
+    if (WRITE_SLOTS) {
+        const int live = s.tok[B];
+        int row = 0;
+        for (int t = gid; t < T; t += gn) {
+            long long slot = -1;
+            int p = -1;
+            if (t < live) {
+                row = row_of(s.tok, row, B, t);
+                if (s.ok[row] == 1) {
+                    p = s.len[row] + t - s.tok[row];
+                    slot = slot_of(row, t - s.tok[row]);
+                }
+            }
+            a.slots[t] = slot;
+            if (a.pos) a.pos[t] = p;
+        }
+    }
+}
+
+// The slots and positions of a step with many tokens.  Every CTA redoes the prefix sum of the new
+// tokens; a sequence's first slot says whether it is served, and its position in its block with the
+// length gives the others.  That first slot is written again with the same value, so its readers
+// in other CTAs need no order.
+__global__ void __launch_bounds__(512) step_slots_kernel(const StepArgs a) {
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ long long ws64[32];
+    int *start = reinterpret_cast<int *>(smem_raw), *base = start + a.B;  // base: position of the first new token, -1: not served
+    const int tid = threadIdx.x, nt = blockDim.x, B = a.B, M = a.M, N = a.N, T = a.T;
+    pdl_wait();
+    pdl_release_dependents();
+    const int per = (B + nt - 1) / nt, b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    long long tok = 0, all;
+    for (int b = b0; b < b1; ++b) tok += max(__ldcg(a.news + b), 0);
+    tok = block_scan(tok, ws64, &all) - tok;
+    for (int b = b0; b < b1; ++b) {
+        const int n = __ldcg(a.news + b);
+        start[b] = (int)min(tok, (long long)T + 1);
+        base[b] = n > 0 && tok < T && __ldcg(a.slots + tok) >= 0 ? __ldcg(a.lens_out + b) - n : -1;
+        tok += max(n, 0);
+    }
+    __syncthreads();
+    const int live = (int)min(all, (long long)T);
     int row = 0;
-    for (int t = gid; t < T; t += gn) {
+    for (int t = blockIdx.x * nt + tid; t < T; t += gridDim.x * nt) {
         long long slot = -1;
         int p = -1;
         if (t < live) {
-            row = row_of(s.tok, row, B, t);
-            if (s.ok[row] == 1) {
-                const int L = s.len[row];
-                p = L + t - s.tok[row];
-                const int k = p / kBlockSize - blocks_of(L);  // < 0: in the block that was partly filled
-                const int x = k < 0 ? s.last[row] : __ldcg(a.free_blocks + count - 1 - s.need[row] - k);
+            row = row_of(start, row, B, t);
+            if (base[row] >= 0) {
+                p = base[row] + t - start[row];
+                const int x = __ldcg(a.tables + (size_t)row * M + p / kBlockSize);
                 slot = x >= 0 && x < N ? (long long)x * kBlockSize + p % kBlockSize : -1;
             }
         }
@@ -281,25 +399,49 @@ __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
     }
 }
 
+// Calls f once per device (again where it failed).
+template <typename F>
+bool set_once(std::atomic<unsigned long long> &done, F f) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev < 64 && (done.load() & bit)) return true;
+    if (!f()) return false;
+    done.fetch_or(bit);
+    return true;
+}
+
+// Raise a kernel's shared-memory limit to `bytes`.
+template <typename K>
+bool raise_smem(K *kern, size_t bytes, std::atomic<unsigned long long> &done) {
+    return set_once(done, [&] {
+        return cudaFuncSetAttribute(reinterpret_cast<const void *>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)bytes) == cudaSuccess;
+    });
+}
+
 }  // namespace
 
 int launch_step_tables(const StepArgs &a, cudaStream_t st) {
-    // A step with few tokens runs on one CTA: a cluster's barriers would only add latency.
-    const int ncta = a.T > 4096 ? 8 : 1;
-    const int threads = a.B <= 256 && a.T <= 1024 ? 256 : 1024;
+    // A step with few tokens is one launch of one CTA: a cluster's barriers and a second launch
+    // would only add latency.
+    const bool few = a.T <= 4096;
+    // (16 CTAs, beyond the portable 8: the steps with prompts hand out thousands of blocks.)
+    const int ncta = few ? 1 : 16;
+    if (!few) {
+        static std::atomic<unsigned long long> wide;
+        if (!set_once(wide, [] {
+                return cudaFuncSetAttribute(reinterpret_cast<const void *>(step_tables_kernel<false>),
+                                            cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+            }))
+            return PA_ERR_CUDA;
+    }
+    const int threads = a.B <= 256 && few ? 256 : 1024;
     const size_t smem = Smem::bytes(a.B);
+    auto kern = few ? step_tables_kernel<true> : step_tables_kernel<false>;
     if (smem > 48 * 1024) {
-        static std::atomic<unsigned long long> done{0};  // devices whose limit is raised
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess) return PA_ERR_CUDA;
-        const unsigned long long bit = 1ull << (dev & 63);
-        if (dev > 63 || !(done.load() & bit)) {
-            if (cudaFuncSetAttribute(reinterpret_cast<const void *>(step_tables_kernel),
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)Smem::bytes(PA_STEP_MAX_SEQS)) != cudaSuccess)
-                return PA_ERR_CUDA;
-            done.fetch_or(bit);
-        }
+        static std::atomic<unsigned long long> done[2];
+        if (!raise_smem(kern, Smem::bytes(PA_STEP_MAX_SEQS), done[few])) return PA_ERR_CUDA;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ncta);
@@ -314,7 +456,18 @@ int launch_step_tables(const StepArgs &a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, step_tables_kernel, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return PA_ERR_CUDA;
+    if (few) return PA_OK;
+    const size_t smem2 = (size_t)a.B * 8;
+    if (smem2 > 48 * 1024) {
+        static std::atomic<unsigned long long> done2;
+        if (!raise_smem(step_slots_kernel, (size_t)PA_STEP_MAX_SEQS * 8, done2)) return PA_ERR_CUDA;
+    }
+    const int64_t ctas = ((int64_t)a.T + 2047) / 2048;
+    return launch_pdl(step_slots_kernel, dim3((unsigned)(ctas < 2 * 148 ? ctas : 2 * 148)), dim3(512), smem2, st, a) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 }  // namespace pa

@@ -238,6 +238,31 @@ def test_counts_of_shared_blocks():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("refs", [False, True])
+def test_rows_that_are_not_served_in_a_step_of_many_tokens(refs):
+    """The slots of a long token buffer are written by a launch of their own."""
+    rng = np.random.default_rng(6)
+    hit = 0
+    for i in range(6):
+        t, l, n, f, c, r = random_step(rng, 200, 40, 600, refs, spare=0.15 * i, bad=True)
+        total = int(np.maximum(n, 0).sum())
+        w = check(t, l, n, f, c, max(4097, total - 300 * (i & 1)), r, in_place=bool(i & 2))
+        hit |= w[-1]
+    assert hit & pa.PA_EFLAG_OUT_OF_BLOCKS and hit & pa.PA_EFLAG_BAD_LENGTH
+
+
+@pytest.mark.gpu
+def test_entries_outside_the_pool_on_the_list():
+    for T in (40, 5000):
+        t, free = np.full((3, 4), -1, np.int32), np.array([5, 9, -1, 4, 8, 2], np.int32)
+        got = run_kernel(t, np.array([0, 16, 0], np.int32), np.array([20, 1, 16], np.int32), free, 5, T)
+        assert got[-1] == pa.PA_EFLAG_BAD_BLOCK
+        assert got[0][0, 1] == 4 and got[0][1, 1] == -1 and got[0][2, 0] == 9 and got[3][0] == 1
+        assert (got[5] < 6 * BS).all() and (got[5][:16] == -1).all() and got[5][20] == -1
+        assert got[1].tolist() == [20, 17, 16]
+
+
+@pytest.mark.gpu
 def test_empty_batch_and_no_slots():
     e = np.zeros((0, 3), np.int32)
     z = np.zeros(0, np.int32)
