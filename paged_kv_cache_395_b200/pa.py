@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -115,9 +116,10 @@ def _load():
     L.pa_quantize_int4.argtypes = [P, i32, P, P, i64, i32, i32, i32, P]
     L.pa_step_tables.argtypes = [P] * 11 + [i32, i32, i64, i64, i32, P]
     L.pa_block_bounds.argtypes = [P] * 7 + [i32] * 5 + [i64, i64, i32, P]
-    L.pa_select_blocks.argtypes = [P] * 7 + [ctypes.POINTER(PaSparseParams), P]
-    L.pa_decode_selected.argtypes = [P] * 8 + [f32, ctypes.POINTER(PaSparseParams), P]
-    L.pa_decode_sparse.argtypes = [P] * 10 + [f32, ctypes.POINTER(PaSparseParams), P]
+    # pa_sparse_params as packed bytes, or a pointer to PaSparseParams
+    L.pa_select_blocks.argtypes = [P] * 9
+    L.pa_decode_selected.argtypes = [P] * 8 + [f32, P, P]
+    L.pa_decode_sparse.argtypes = [P] * 10 + [f32, P, P]
     L.pa_get_error_flags.argtypes = [ctypes.POINTER(ctypes.c_uint), i32, P]
     L.pa_status_string.argtypes = [i32]
     L.pa_status_string.restype = ctypes.c_char_p
@@ -436,24 +438,36 @@ def pa_quantize_int4(src_cache, dst_cache, scales, stream=None):
                                 _ptr(scales), N, H, d, bs, _stream(stream)), "pa_quantize_int4")
 
 
-def _here(*ts) -> int:
-    """The current device, where every tensor has to be: a call launches on its stream."""
-    devs = {t.get_device() for t in ts if t is not None}
+# The calls below run once per layer of a decode step, so their checks are written to be
+# cheap: one expression over a call's tensors, and only when it fails the search for the
+# message.
+_I32, _I64, _F32, _I8 = torch.int32, torch.int64, torch.float32, torch.int8
+_get_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_SPARSE_PARAMS = struct.Struct("@6iq3iPP5i4x")  # pa_sparse_params
+assert _SPARSE_PARAMS.size == ctypes.sizeof(PaSparseParams)
+
+
+def _refuse(tensors, rules):
+    """Raises the ValueError of the first thing that is wrong: devices, then rules
+    (broken, message)."""
+    devs = [t.get_device() for t in tensors if t is not None]
     if -1 in devs:
         raise ValueError("all tensors must be CUDA tensors")
-    dev = torch.cuda.current_device()
-    if devs != {dev}:
+    if any(d != _get_device() for d in devs):
         raise ValueError("all tensors must be on the current device")
-    return dev
+    for broken, message in rules:
+        if broken:
+            raise ValueError(message)
+    raise ValueError("invalid arguments")
 
 
-def _stream_on(dev: int, stream):
-    """The raw handle of the stream, by default the device's current one."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
+def _on(dev, *ts):
+    """Whether the optional tensors ts are absent or on device dev and contiguous."""
+    for t in ts:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            return False
+    return True
 
 
 def pa_step_tables(block_tables, seq_lens, new_lens, free_blocks, free_count, slot_mapping, seq_lens_out=None,
@@ -468,37 +482,39 @@ def pa_step_tables(block_tables, seq_lens, new_lens, free_blocks, free_count, sl
     free_count_out the inputs are updated in place."""
     lens_out = seq_lens if seq_lens_out is None else seq_lens_out
     count_out = free_count if free_count_out is None else free_count_out
-    dev = _here(block_tables, seq_lens, new_lens, lens_out, free_blocks, free_count, count_out, slot_mapping, positions,
-                row_starts, refcounts)
-    i32 = torch.int32
     B, M = block_tables.shape
     N, T = free_blocks.numel(), slot_mapping.numel()
-    for t, n, name in ((block_tables, B * M, "block_tables"), (seq_lens, B, "seq_lens"), (new_lens, B, "new_lens"),
-                       (lens_out, B, "seq_lens_out"), (free_blocks, N, "free_blocks"), (free_count, 1, "free_count"),
-                       (count_out, 1, "free_count_out"), (positions, T, "positions"), (row_starts, B + 1, "row_starts"),
-                       (refcounts, N, "refcounts")):
-        if t is not None and (t.dtype != i32 or t.numel() != n or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous int32 with {n} elements")
-    if slot_mapping.dtype != torch.int64 or not slot_mapping.is_contiguous():
-        raise ValueError("slot_mapping must be contiguous int64")
-    _check(lib.pa_step_tables(_addr(block_tables), _addr(seq_lens), _addr(new_lens), _addr(lens_out), _addr(free_blocks),
-                              _addr(free_count), _addr(count_out), _addr(refcounts), _addr(slot_mapping),
-                              _addr(positions), _addr(row_starts), B, M, N, T, BLOCK_SIZE, _stream_on(dev, stream)),
-           "pa_step_tables")
+    dev = block_tables.get_device()
+    good = dev >= 0 and dev == _get_device() and slot_mapping.dtype is _I64 and slot_mapping.get_device() == dev and \
+        slot_mapping.is_contiguous() and block_tables.dtype is _I32 and block_tables.is_contiguous()
+    for t, n in ((seq_lens, B), (new_lens, B), (lens_out, B), (free_blocks, N), (free_count, 1), (count_out, 1),
+                 (positions, T), (row_starts, B + 1), (refcounts, N)):
+        if t is not None and (t.numel() != n or t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous()):
+            good = False
+    if not good:
+        ints = dict(block_tables=(block_tables, B * M), seq_lens=(seq_lens, B), new_lens=(new_lens, B),
+                    seq_lens_out=(lens_out, B), free_blocks=(free_blocks, N), free_count=(free_count, 1),
+                    free_count_out=(count_out, 1), positions=(positions, T), row_starts=(row_starts, B + 1),
+                    refcounts=(refcounts, N))
+        _refuse([t for t, _ in ints.values()] + [slot_mapping],
+                [(t is not None and (t.dtype != _I32 or t.numel() != n or not t.is_contiguous()),
+                  f"{name} must be contiguous int32 with {n} elements") for name, (t, n) in ints.items()] +
+                [(True, "slot_mapping must be contiguous int64")])
+    rc = lib.pa_step_tables(
+        block_tables.data_ptr(), seq_lens.data_ptr(), new_lens.data_ptr(), lens_out.data_ptr(), free_blocks.data_ptr(),
+        free_count.data_ptr(), count_out.data_ptr(), None if refcounts is None else refcounts.data_ptr(),
+        slot_mapping.data_ptr(), None if positions is None else positions.data_ptr(),
+        None if row_starts is None else row_starts.data_ptr(), B, M, N, T, BLOCK_SIZE,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pa_step_tables")
 
 
-def _contiguous(**ts):
-    for name, t in ts.items():
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-
-
-def _boxes(bounds, bound_scales, N, H, d):
-    """bounds int8 [N][H_kv][2][d] and their scales fp32 [N][H_kv]."""
-    if bounds.dtype != torch.int8 or tuple(bounds.shape) != (N, H, 2, d) or not bounds.is_contiguous():
-        raise ValueError("bounds must be contiguous int8 [N][H_kv][2][d]")
-    if bound_scales.dtype != torch.float32 or tuple(bound_scales.shape) != (N, H) or not bound_scales.is_contiguous():
-        raise ValueError("bound_scales must be contiguous float32 [N][H_kv]")
+def _box_rules(bounds, bound_scales, N, H, d):
+    return [(bounds.dtype != _I8 or tuple(bounds.shape) != (N, H, 2, d) or not bounds.is_contiguous(),
+             "bounds must be contiguous int8 [N][H_kv][2][d]"),
+            (bound_scales.dtype != _F32 or tuple(bound_scales.shape) != (N, H) or not bound_scales.is_contiguous(),
+             "bound_scales must be contiguous float32 [N][H_kv]")]
 
 
 def pa_block_bounds(bounds, bound_scales, key_cache, block_tables, seq_lens, max_new_tokens, first_lens=None,
@@ -508,43 +524,56 @@ def pa_block_bounds(bounds, bound_scales, key_cache, block_tables, seq_lens, max
     at most ceil(max_new_tokens / 16) of them (see include/pa.h).  bounds int8
     [N][H_kv][2][d], bound_scales fp32 [N][H_kv] (updated in place); key_cache
     [N][H_kv][16][d] fp32/fp16/bf16, or int8 with k_scales [N][H_kv]."""
-    dev = _here(bounds, bound_scales, key_cache, block_tables, seq_lens, first_lens, k_scales)
     N, H, bs, d = key_cache.shape
     B, M = block_tables.shape
-    _boxes(bounds, bound_scales, N, H, d)
-    _contiguous(key_cache=key_cache, block_tables=block_tables, k_scales=k_scales)
-    i32 = torch.int32
-    if block_tables.dtype != i32:
-        raise ValueError("block_tables must be int32")
-    for t, name in ((seq_lens, "seq_lens"), (first_lens, "first_lens")):
-        if t is not None and (t.dtype != i32 or t.numel() != B or not t.is_contiguous()):
-            raise ValueError(f"{name} must be contiguous int32 with {B} elements")
-    if k_scales is not None and (k_scales.dtype != torch.float32 or tuple(k_scales.shape) != (N, H)):
-        raise ValueError("k_scales must be float32 [N][H_kv]")
-    _check(lib.pa_block_bounds(_addr(bounds), _addr(bound_scales), _addr(key_cache), _addr(k_scales),
-                               _addr(block_tables), _addr(first_lens), _addr(seq_lens), B, H, d, bs, M, N,
-                               int(max_new_tokens), dtype_code(key_cache.dtype), _stream_on(dev, stream)),
-           "pa_block_bounds")
+    dev = key_cache.get_device()
+    if not (dev >= 0 and dev == _get_device() and key_cache.is_contiguous() and bounds.dtype is _I8 and
+            bounds.shape == (N, H, 2, d) and bound_scales.dtype is _F32 and bound_scales.shape == (N, H) and
+            block_tables.dtype is _I32 and seq_lens.dtype is _I32 and seq_lens.numel() == B and
+            (first_lens is None or (first_lens.dtype is _I32 and first_lens.numel() == B)) and
+            (k_scales is None or (k_scales.dtype is _F32 and k_scales.shape == (N, H))) and
+            _on(dev, bounds, bound_scales, block_tables, seq_lens, first_lens, k_scales)):
+        _refuse([bounds, bound_scales, key_cache, block_tables, seq_lens, first_lens, k_scales],
+                _box_rules(bounds, bound_scales, N, H, d) +
+                [(not key_cache.is_contiguous(), "key_cache must be contiguous"),
+                 (block_tables.dtype != _I32 or not block_tables.is_contiguous(), "block_tables must be contiguous int32")] +
+                [(t is not None and (t.dtype != _I32 or t.numel() != B or not t.is_contiguous()),
+                  f"{name} must be contiguous int32 with {B} elements")
+                 for t, name in ((seq_lens, "seq_lens"), (first_lens, "first_lens"))] +
+                [(True, "k_scales must be contiguous float32 [N][H_kv]")])
+    rc = lib.pa_block_bounds(
+        bounds.data_ptr(), bound_scales.data_ptr(), key_cache.data_ptr(), None if k_scales is None else k_scales.data_ptr(),
+        block_tables.data_ptr(), None if first_lens is None else first_lens.data_ptr(), seq_lens.data_ptr(), B, H, d, bs,
+        M, N, max_new_tokens, _TORCH_DTYPE[key_cache.dtype], _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pa_block_bounds")
 
 
-def _sparse_params(q, H, N, block_tables, seq_lens, selected, num_selected, max_seq_len, sink_blocks, recent_blocks,
-                   kv_dtype, k_scales=None, v_scales=None, flags=0):
-    """Checks what the block-sparse calls share; q [B][H_q][d] or [B][Q][H_q][d]."""
-    shape = q.shape
-    Q = shape[1] if len(shape) == 4 else 1
-    B, Hq, d = shape[0], shape[-2], shape[-1]
+def _list_rules(q, H, block_tables, seq_lens, selected, num_selected):
+    lead = q.shape[:-2]
+    return [(q.dim() not in (3, 4), "q must be [B][H_q][d] or [B][Q][H_q][d]"),
+            (tuple(selected.shape[:-1]) != lead + (H,) or tuple(num_selected.shape) != lead + (H,),
+             "selected must be q's leading sizes, then [H_kv][K], and num_selected the same without K"),
+            (block_tables.dim() != 2 or block_tables.shape[0] != q.shape[0] or seq_lens.numel() != q.shape[0],
+             "block_tables must be [B][M] and seq_lens [B]"),
+            (any(t.dtype != _I32 for t in (selected, num_selected, block_tables, seq_lens)),
+             "selected, num_selected, block_tables and seq_lens must be int32")] + \
+        [(not t.is_contiguous(), f"{name} must be contiguous")
+         for t, name in ((q, "q"), (selected, "selected"), (num_selected, "num_selected"),
+                         (block_tables, "block_tables"), (seq_lens, "seq_lens"))]
+
+
+def _lists_good(q, shape, H, dev, block_tables, seq_lens, selected, num_selected):
+    """What the block-sparse calls ask of q (of that shape), the lists, tables and lengths."""
     lead = shape[:-2]
-    K = selected.shape[-1]
-    i32 = torch.int32
-    if len(shape) not in (3, 4) or selected.shape[:-1] != lead + (H,) or num_selected.shape != lead + (H,):
-        raise ValueError("selected must be q's leading sizes, then [H_kv][K], and num_selected the same without K")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or seq_lens.numel() != B:
-        raise ValueError("block_tables must be [B][M] and seq_lens [B]")
-    if not (selected.dtype == num_selected.dtype == block_tables.dtype == seq_lens.dtype == i32):
-        raise ValueError("selected, num_selected, block_tables and seq_lens must be int32")
-    _contiguous(q=q, selected=selected, num_selected=num_selected, block_tables=block_tables, seq_lens=seq_lens)
-    return PaSparseParams(B, Hq, H, d, BLOCK_SIZE, block_tables.shape[1], N, int(max_seq_len), dtype_code(q.dtype),
-                          kv_dtype, _addr(k_scales), _addr(v_scales), Q, K, int(sink_blocks), int(recent_blocks), flags)
+    return (dev >= 0 and dev == _get_device() and 3 <= len(shape) <= 4 and
+            selected.shape[:-1] == lead + (H,) and num_selected.shape == lead + (H,) and
+            block_tables.dim() == 2 and len(block_tables) == shape[0] and seq_lens.numel() == shape[0] and
+            selected.dtype is _I32 and num_selected.dtype is _I32 and block_tables.dtype is _I32 and
+            seq_lens.dtype is _I32 and q.is_contiguous() and selected.is_contiguous() and
+            num_selected.is_contiguous() and block_tables.is_contiguous() and seq_lens.is_contiguous() and
+            selected.get_device() == num_selected.get_device() == block_tables.get_device() ==
+            seq_lens.get_device() == dev)
 
 
 def pa_select_blocks(selected, num_selected, q, bounds, bound_scales, block_tables, seq_lens, max_seq_len,
@@ -553,28 +582,50 @@ def pa_select_blocks(selected, num_selected, q, bounds, bound_scales, block_tabl
     selected int32 [B][H_kv][K] (or [B][Q][H_kv][K]), filled with logical blocks,
     ascending, then -1; num_selected int32 without the K.  q [B][H_q][d] or
     [B][Q][H_q][d]; bounds, bound_scales as pa_block_bounds leaves them."""
-    dev = _here(selected, num_selected, q, bounds, bound_scales, block_tables, seq_lens)
+    shape, dev = q.shape, q.get_device()
     N, H = bound_scales.shape
-    _boxes(bounds, bound_scales, N, H, q.shape[-1])
-    p = _sparse_params(q, H, N, block_tables, seq_lens, selected, num_selected, max_seq_len, sink_blocks,
-                       recent_blocks, dtype_code(q.dtype))
-    _check(lib.pa_select_blocks(selected.data_ptr(), num_selected.data_ptr(), q.data_ptr(), bounds.data_ptr(),
-                                bound_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(),
-                                ctypes.byref(p), _stream_on(dev, stream)), "pa_select_blocks")
+    d = shape[-1]
+    if not (_lists_good(q, shape, H, dev, block_tables, seq_lens, selected, num_selected) and bounds.dtype is _I8 and
+            bounds.shape == (N, H, 2, d) and bound_scales.dtype is _F32 and _on(dev, bounds, bound_scales)):
+        _refuse([selected, num_selected, q, bounds, bound_scales, block_tables, seq_lens],
+                _list_rules(q, H, block_tables, seq_lens, selected, num_selected) +
+                _box_rules(bounds, bound_scales, N, H, d))
+    dt = _TORCH_DTYPE[q.dtype]
+    p = _SPARSE_PARAMS.pack(shape[0], shape[-2], H, d, BLOCK_SIZE, block_tables.shape[1], N, max_seq_len, dt, dt, 0, 0,
+                            shape[1] if len(shape) == 4 else 1, selected.shape[-1], sink_blocks, recent_blocks, 0)
+    rc = lib.pa_select_blocks(selected.data_ptr(), num_selected.data_ptr(), q.data_ptr(), bounds.data_ptr(),
+                              bound_scales.data_ptr(), block_tables.data_ptr(), seq_lens.data_ptr(), p,
+                              _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pa_select_blocks")
 
 
-def _sparse_decode(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, max_seq_len,
-                   sink_blocks, recent_blocks, k_scales, v_scales):
-    N, H, bs, d = key_cache.shape
-    if value_cache.shape != key_cache.shape or value_cache.dtype != key_cache.dtype or bs != BLOCK_SIZE or \
-            d != q.shape[-1]:
-        raise ValueError("caches must be [N][H_kv][16][d] of one dtype, with q's d")
-    _contiguous(out=out, key_cache=key_cache, value_cache=value_cache, k_scales=k_scales, v_scales=v_scales)
-    for t in (k_scales, v_scales):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (N, H)):
-            raise ValueError("scales must be float32 [N][H_kv]")
-    return _sparse_params(q, H, N, block_tables, seq_lens, selected, num_selected, max_seq_len, sink_blocks,
-                          recent_blocks, dtype_code(key_cache.dtype), k_scales, v_scales, _out_flag(out, q))
+def _sparse_decode_params(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, max_seq_len,
+                          sink_blocks, recent_blocks, k_scales, v_scales):
+    """Checks the attention's operands; the packed pa_sparse_params, N, H_kv and the device."""
+    shape, dev = q.shape, q.get_device()
+    N, H, bs, d = kshape = key_cache.shape
+    f32 = out.dtype is not q.dtype
+    if not (_lists_good(q, shape, H, dev, block_tables, seq_lens, selected, num_selected) and
+            value_cache.shape == kshape and value_cache.dtype is key_cache.dtype and bs == BLOCK_SIZE and
+            shape[-1] == d and out.shape == shape and (not f32 or out.dtype is _F32) and
+            (k_scales is None or (k_scales.dtype is _F32 and k_scales.shape == (N, H))) and
+            (v_scales is None or (v_scales.dtype is _F32 and v_scales.shape == (N, H))) and
+            _on(dev, out, key_cache, value_cache, k_scales, v_scales)):
+        _refuse([out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, k_scales, v_scales],
+                _list_rules(q, H, block_tables, seq_lens, selected, num_selected) +
+                [(value_cache.shape != kshape or value_cache.dtype != key_cache.dtype or bs != BLOCK_SIZE or
+                  shape[-1] != d, "caches must be [N][H_kv][16][d] of one dtype, with q's d"),
+                 (out.shape != shape or out.dtype not in (q.dtype, _F32),
+                  "out must match q in shape, and in dtype or be float32")] +
+                [(not t.is_contiguous(), f"{name} must be contiguous")
+                 for t, name in ((out, "out"), (key_cache, "key_cache"), (value_cache, "value_cache"))] +
+                [(True, "scales must be contiguous float32 [N][H_kv]")])
+    p = _SPARSE_PARAMS.pack(shape[0], shape[-2], H, d, bs, block_tables.shape[1], N, max_seq_len, _TORCH_DTYPE[q.dtype],
+                            _TORCH_DTYPE[key_cache.dtype], 0 if k_scales is None else k_scales.data_ptr(),
+                            0 if v_scales is None else v_scales.data_ptr(), shape[1] if len(shape) == 4 else 1,
+                            selected.shape[-1], sink_blocks, recent_blocks, PA_DECODE_OUT_F32 if f32 else 0)
+    return p, N, H, dev
 
 
 def pa_decode_selected(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, scale,
@@ -582,13 +633,14 @@ def pa_decode_selected(out, q, key_cache, value_cache, block_tables, seq_lens, s
     """Decode attention over the blocks that selected / num_selected list (int32
     [B][H_kv][K], [B][H_kv], or with a Q after the B; see include/pa.h).  out, q, caches,
     block_tables and seq_lens as in pa_decode; int8 caches with their scales."""
-    dev = _here(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, k_scales, v_scales)
-    p = _sparse_decode(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, max_seq_len,
-                       0, 1, k_scales, v_scales)
-    _check(lib.pa_decode_selected(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-                                  block_tables.data_ptr(), seq_lens.data_ptr(), selected.data_ptr(),
-                                  num_selected.data_ptr(), scale, ctypes.byref(p), _stream_on(dev, stream)),
-           "pa_decode_selected")
+    p, _, _, dev = _sparse_decode_params(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected,
+                                         max_seq_len, 0, 1, k_scales, v_scales)
+    rc = lib.pa_decode_selected(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                block_tables.data_ptr(), seq_lens.data_ptr(), selected.data_ptr(),
+                                num_selected.data_ptr(), scale, p,
+                                _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pa_decode_selected")
 
 
 def pa_decode_sparse(out, q, key_cache, value_cache, bounds, bound_scales, block_tables, seq_lens, selected,
@@ -596,15 +648,17 @@ def pa_decode_sparse(out, q, key_cache, value_cache, bounds, bound_scales, block
                      stream=None):
     """pa_select_blocks and pa_decode_selected in one call: selected and num_selected
     are filled and attended to.  Arguments as in those."""
-    dev = _here(out, q, key_cache, value_cache, bounds, bound_scales, block_tables, seq_lens, selected, num_selected,
-                k_scales, v_scales)
-    p = _sparse_decode(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, max_seq_len,
-                       sink_blocks, recent_blocks, k_scales, v_scales)
-    _boxes(bounds, bound_scales, p.num_blocks, p.num_kv_heads, p.head_dim)
-    _check(lib.pa_decode_sparse(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
-                                bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(),
-                                seq_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), scale,
-                                ctypes.byref(p), _stream_on(dev, stream)), "pa_decode_sparse")
+    p, N, H, dev = _sparse_decode_params(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected,
+                                         max_seq_len, sink_blocks, recent_blocks, k_scales, v_scales)
+    if not (bounds.dtype is _I8 and bounds.shape == (N, H, 2, q.shape[-1]) and bound_scales.dtype is _F32 and
+            bound_scales.shape == (N, H) and _on(dev, bounds, bound_scales)):
+        _refuse([bounds, bound_scales], _box_rules(bounds, bound_scales, N, H, q.shape[-1]))
+    rc = lib.pa_decode_sparse(out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                              bounds.data_ptr(), bound_scales.data_ptr(), block_tables.data_ptr(),
+                              seq_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), scale, p,
+                              _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "pa_decode_sparse")
 
 
 def pa_get_error_flags(reset: bool = True, stream=None) -> int:
