@@ -11,9 +11,14 @@
 // the score reads 1/32 of what dense attention would.
 //
 // The row's keys (scores as ordered whole numbers) are gathered in the shared memory of the
-// cluster's first CTA, which alone picks: the cut is found by histograms of 256 bins over
-// the range that still holds it, starting at the scores' own range (two or three rounds;
-// four at most), and the picks are written in index order.
+// cluster's first CTA, which alone picks: a histogram of 256 bins over the scores' range finds
+// the bin that holds the cut, that bin's few keys are ranked against each other (or, when equal
+// scores make them many, the histogram is taken again over the bin), and every thread writes the
+// picks of its run of the row in order.
+//
+// What bounds it is the latency of dependent loads and barriers, not bytes: so nothing that is
+// asked for first (table entries, q) waits for the row's length, the boxes of a warp's first tile
+// are on their way while q's codes are made, and later tiles are fetched a step ahead.
 #pragma once
 #include <cooperative_groups.h>
 
@@ -34,7 +39,8 @@ __device__ __forceinline__ void imma(int (&d)[4], uint32_t a0, uint32_t a1, uint
 template <int D>
 struct SelectSmem {
     static constexpr int QROW = 2 * D + 64;
-    static constexpr int MISC = 4 * (256 + 4 * 32 + 16);
+    static constexpr int CAND = 512;  // keys of the cut's bin that are ranked directly
+    static constexpr int MISC = 4 * (256 + CAND + 2 * 32 + 16);
     static __host__ __device__ int heads(int G) { return (G + 7) / 8 * 8; }
     static __host__ __device__ size_t bytes(int G, int nblk) {
         return (size_t)heads(G) * (QROW + 4) + MISC + (size_t)((nblk + 31) / 32 * 32) * 4;
@@ -47,106 +53,173 @@ __device__ __forceinline__ int sparse_row_len(const SparseArgs &a, int r, int &b
     return max(min(max(a.lens[b], 0), a.max_len) - a.Q + 1 + (r - b * a.Q), 0);
 }
 
-// Every CTA of the cluster calls this with all its threads (a multiple of 32, 256 or more).  On
-// return the cluster's first CTA has written the row's list; nothing is synchronised after that.
-template <typename T, int D>
+// Every CTA of the cluster calls this with all its NT threads.  On return the cluster's first CTA has
+// written the row's list; nothing is synchronised after that.
+template <typename T, int D, int NT>
 __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta, unsigned char *smem) {
     using S = SelectSmem<D>;
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+    constexpr int nw = NT / 32, EL = D / 32;       // warps; dims of q per lane
+    constexpr bool AHEAD = NT > 256 && D <= 128;   // boxes of the next tile in registers
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const int NH = S::heads(a.G), K = a.K;
+    const float kInf = __int_as_float(0x7f800000);
     int8_t *qc = reinterpret_cast<int8_t *>(smem);
     float *qs = reinterpret_cast<float *>(smem + NH * S::QROW);
     uint32_t *hist = reinterpret_cast<uint32_t *>(qs + NH);
-    uint32_t *wa = hist + 256, *wb = wa + 32, *wc = wb + 32, *misc = wc + 64;
+    uint32_t *cand = hist + 256, *wa = cand + S::CAND, *wb = wa + 32, *misc = wb + 32;
     uint32_t *keys = reinterpret_cast<uint32_t *>(smem + NH * (S::QROW + 4) + S::MISC);
 
+    // ---- asked for at once: the table entries of the warp's first tile, q's first heads, the length ----
+    // tile i of the warp: blocks 16 ((i nw + warp) ncta + rank) on
+    const int32_t *table = a.tables + (size_t)(r / a.Q) * a.M;
+    const int step = 16 * nw * ncta;
+    int j0 = 16 * (warp * ncta + rank);
+    auto entries = [&](int j) { return lane < 16 && j + lane < a.M ? __ldcg(table + j + lane) : -1; };
+    int id = entries(j0);
+    constexpr int QB = 4;  // heads per warp and batch
+    const T *q0 = reinterpret_cast<const T *>(a.q) + ((size_t)r * a.Hq + (size_t)h * a.G) * D + lane * EL;
+    const bool qvec = ((uintptr_t)a.q & 15) == 0;
+    float qx[QB][EL];
+    auto q_load = [&](int g0) {
+#pragma unroll
+        for (int i = 0; i < QB; ++i) {
+            const int hd = g0 + warp + i * nw;
+            const T *q = q0 + (size_t)hd * D;
+            if (hd >= a.G) {
+#pragma unroll
+                for (int e = 0; e < EL; ++e) qx[i][e] = 0.f;
+            } else if (qvec) {
+                uint32_t w[EL * sizeof(T) / 4];
+#pragma unroll
+                for (int e = 0; e < (int)(EL * sizeof(T) / 4); ++e) w[e] = __ldcg(reinterpret_cast<const uint32_t *>(q) + e);
+                to_float<T, EL>(w, qx[i]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < EL; ++e) qx[i][e] = Cvt<T>::to_f(q[e]);
+            }
+        }
+    };
+    q_load(0);
     int b;
     const int L = sparse_row_len(a, r, b), n = (L + kBlockSize - 1) / kBlockSize;
     int32_t *out = a.sel + ((size_t)r * a.H + h) * K;
     if (n <= K) {  // the same in every CTA of the cluster
         if (rank == 0) {
-            for (int i = tid; i < K; i += nt) out[i] = i < n ? i : -1;
+            for (int i = tid; i < K; i += NT) out[i] = i < n ? i : -1;
             if (tid == 0) a.nsel[(size_t)r * a.H + h] = n;
         }
         return;
     }
-
-    // the first CTA's shared memory is written by the others only once that CTA runs: the wait
+    const int f0 = a.sink, f1 = n - a.recent;  // the unforced blocks
+    if (tid < 256) hist[tid] = 0;
+    if (tid == 0) {
+        misc[0] = 0xffffffffu;  // smallest and largest key of the unforced blocks
+        misc[1] = 0;
+        misc[5] = 0;            // candidates
+    }
+    // the first CTA's shared memory is written by the others only once that CTA is here: the wait
     // for this is below, before the first score
-    if (ncta > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    if (ncta > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+
+    // ---- the boxes of 16 blocks: lane (g, c) holds 16-byte pieces c, c + 4, ... of blocks g and g + 8 ----
+    struct Box {
+        uint4 u[D / 32], v[D / 32];
+        float s0, s1;
+        int i0, i1;
+    };
+    auto fetch = [&](int j, int ids, Box &x) {
+        if (lane < 16 && j + lane < n && (ids < 0 || (int64_t)ids >= a.N)) {
+            ids = -1;
+            raise_flag(PA_EFLAG_BAD_BLOCK);
+        }
+        if (j + lane >= n) ids = -1;
+        x.i0 = __shfl_sync(0xffffffffu, ids, g);
+        x.i1 = __shfl_sync(0xffffffffu, ids, g + 8);
+        const size_t t0 = (size_t)max(x.i0, 0) * a.H + h, t1 = (size_t)max(x.i1, 0) * a.H + h;
+        const uint4 *p0 = reinterpret_cast<const uint4 *>(a.bounds + t0 * (2 * D)) + c;
+        const uint4 *p1 = reinterpret_cast<const uint4 *>(a.bounds + t1 * (2 * D)) + c;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            x.u[i] = x.i0 >= 0 ? __ldg(p0 + 4 * i) : make_uint4(0, 0, 0, 0);
+            x.v[i] = x.i1 >= 0 ? __ldg(p1 + 4 * i) : make_uint4(0, 0, 0, 0);
+        }
+        x.s0 = x.i0 >= 0 ? __ldg(a.bscales + t0) : 0.f;
+        x.s1 = x.i1 >= 0 ? __ldg(a.bscales + t1) : 0.f;
+    };
+    Box box;
+    int id_next = entries(j0 + step);
+    if (j0 < n) fetch(j0, id, box);
 
     // ---- codes of q: [min(c, 0) for every dim][max(c, 0) for every dim] per head ----
-    for (int g = warp; g < NH; g += nw) {
-        float x[D / 32], m = 0.f;
-        const T *q = reinterpret_cast<const T *>(a.q) + ((size_t)r * a.Hq + (size_t)h * a.G + g) * D;
+    for (int g0 = 0; g0 < NH; g0 += QB * nw) {
+        if (g0 > 0) q_load(g0);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            x[i] = g < a.G ? Cvt<T>::to_f(q[lane * (D / 32) + i]) : 0.f;
-            // an infinity or NaN gives m = inf: the codes are then 0
-            m = fmaxf(m, fabsf(x[i]) <= 3.402823466e38f ? fabsf(x[i]) : __int_as_float(0x7f800000));
-        }
+        for (int i = 0; i < QB; ++i) {
+            const int hd = g0 + warp + i * nw;
+            if (hd >= NH) break;
+            float m = 0.f;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float s = __fdiv_rn(m, 127.0f);
-        if (!(s < __int_as_float(0x7f800000))) s = 0.f;
-        if (lane == 0) qs[g] = s;
-        int8_t *row = qc + g * S::QROW;
+            for (int e = 0; e < EL; ++e)  // an infinity or NaN gives m = inf: the codes are then 0
+                m = fmaxf(m, fabsf(qx[i][e]) <= 3.402823466e38f ? fabsf(qx[i][e]) : kInf);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            int c = 0;
-            if (s > 0.f) c = max(-127, min(127, __float2int_rn(__fdiv_rn(x[i], s))));
-            row[lane * (D / 32) + i] = (int8_t)min(c, 0);
-            row[D + lane * (D / 32) + i] = (int8_t)max(c, 0);
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            float s = __fdiv_rn(m, 127.0f);
+            if (!(s < kInf)) s = 0.f;
+            if (lane == 0) qs[hd] = s;
+            uint32_t lo[(EL + 3) / 4] = {}, hi[(EL + 3) / 4] = {};
+#pragma unroll
+            for (int e = 0; e < EL; ++e) {
+                int k = 0;
+                if (s > 0.f) k = max(-127, min(127, __float2int_rn(__fdiv_rn(qx[i][e], s))));
+                lo[e / 4] |= (uint32_t)(min(k, 0) & 0xff) << (8 * (e % 4));
+                hi[e / 4] |= (uint32_t)max(k, 0) << (8 * (e % 4));
+            }
+            int8_t *row = qc + hd * S::QROW + lane * EL;
+            if constexpr (EL == 2) {
+                *reinterpret_cast<uint16_t *>(row) = (uint16_t)lo[0];
+                *reinterpret_cast<uint16_t *>(row + D) = (uint16_t)hi[0];
+            } else {
+#pragma unroll
+                for (int e = 0; e < EL / 4; ++e) {
+                    reinterpret_cast<uint32_t *>(row)[e] = lo[e];
+                    reinterpret_cast<uint32_t *>(row + D)[e] = hi[e];
+                }
+            }
         }
     }
     __syncthreads();
 
-    // ---- scores of this CTA's blocks ----
-    const int per = ((n + ncta - 1) / ncta + 15) / 16 * 16, lo = min(n, rank * per), hi = min(n, lo + per);
-    const int g = lane >> 2, c = lane & 3;
-    uint32_t *dst = keys;
+    // ---- scores ----
+    uint32_t *dst = keys, *range = misc;
     if (ncta > 1) {
         dst = cooperative_groups::this_cluster().map_shared_rank(keys, 0);
-        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        range = cooperative_groups::this_cluster().map_shared_rank(misc, 0);
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     }
-    const int32_t *table = a.tables + (size_t)b * a.M;
-    for (int j0 = lo + warp * 16; j0 < hi; j0 += nw * 16) {
-        int id = -1;
-        if (lane < 16 && j0 + lane < hi) {
-            id = table[j0 + lane];
-            if (id < 0 || (int64_t)id >= a.N) {
-                id = -1;
-                raise_flag(PA_EFLAG_BAD_BLOCK);
-            }
-        }
-        const int i0 = __shfl_sync(0xffffffffu, id, g), i1 = __shfl_sync(0xffffffffu, id, g + 8);
-        const size_t t0 = (size_t)max(i0, 0) * a.H + h, t1 = (size_t)max(i1, 0) * a.H + h;
-        const uint4 *p0 = reinterpret_cast<const uint4 *>(a.bounds + t0 * (2 * D)) + c;
-        const uint4 *p1 = reinterpret_cast<const uint4 *>(a.bounds + t1 * (2 * D)) + c;
-        uint4 u[D / 32], v[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            u[i] = i0 >= 0 ? __ldg(p0 + 4 * i) : make_uint4(0, 0, 0, 0);
-            v[i] = i1 >= 0 ? __ldg(p1 + 4 * i) : make_uint4(0, 0, 0, 0);
-        }
-        const float s0 = i0 >= 0 ? __ldg(a.bscales + t0) : 0.f, s1 = i1 >= 0 ? __ldg(a.bscales + t1) : 0.f;
-        float m0 = __int_as_float(0xff800000), m1 = m0;
+    uint32_t kl = 0xffffffffu, kh = 0;
+    for (; j0 < n; j0 += step) {
+        Box next;
+        const int id2 = j0 + step < n ? id_next : -1;
+        if (j0 + 2 * step < n) id_next = entries(j0 + 2 * step);
+        if (AHEAD && j0 + step < n) fetch(j0 + step, id2, next);
+        float m0 = -kInf, m1 = m0;
         for (int hb = 0; hb < NH; hb += 8) {
-            int d[4] = {0, 0, 0, 0};
+            int d[2][4] = {};
             const uint4 *bq = reinterpret_cast<const uint4 *>(qc + (hb + g) * S::QROW) + c;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 const uint4 w = bq[4 * i];
-                imma(d, u[i].x, v[i].x, u[i].y, v[i].y, w.x, w.y);
-                imma(d, u[i].z, v[i].z, u[i].w, v[i].w, w.z, w.w);
+                imma(d[0], box.u[i].x, box.v[i].x, box.u[i].y, box.v[i].y, w.x, w.y);
+                imma(d[1], box.u[i].z, box.v[i].z, box.u[i].w, box.v[i].w, w.z, w.w);
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int col = hb + 2 * c + e;
                 if (col < a.G) {
                     // + 0: a product that underflows to -0 becomes +0
-                    m0 = fmaxf(m0, __fmul_rn(__fmul_rn((float)d[e], s0), qs[col]) + 0.f);
-                    m1 = fmaxf(m1, __fmul_rn(__fmul_rn((float)d[2 + e], s1), qs[col]) + 0.f);
+                    const float sq = qs[col];
+                    m0 = fmaxf(m0, __fmul_rn(__fmul_rn((float)(d[0][e] + d[1][e]), box.s0), sq) + 0.f);
+                    m1 = fmaxf(m1, __fmul_rn(__fmul_rn((float)(d[0][2 + e] + d[1][2 + e]), box.s1), sq) + 0.f);
                 }
             }
         }
@@ -157,12 +230,25 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
         }
         if (c < 2) {
             const int j = j0 + g + 8 * c;
-            const float s = c ? s1 : s0;
-            uint32_t k = __float_as_uint(s < __int_as_float(0x7f800000) ? (c ? m1 : m0) : __int_as_float(0x7f800000));
+            uint32_t k = __float_as_uint((c ? box.s1 : box.s0) < kInf ? (c ? m1 : m0) : kInf);
             k ^= (k >> 31) ? 0xffffffffu : 0x80000000u;  // ordered as whole numbers
-            if ((c ? i1 : i0) < 0) k = 0;
-            if (j < hi) dst[j] = k;
+            if ((c ? box.i1 : box.i0) < 0) k = 0;
+            if (j < n) dst[j] = k;
+            if (j >= f0 && j < f1) {
+                kl = min(kl, k);
+                kh = max(kh, k);
+            }
         }
+        if (AHEAD)
+            box = next;
+        else if (j0 + step < n)
+            fetch(j0 + step, id2, box);
+    }
+    kl = __reduce_min_sync(0xffffffffu, kl);
+    kh = __reduce_max_sync(0xffffffffu, kh);
+    if (lane == 0 && kl <= kh) {
+        atomicMin(range, kl);
+        atomicMax(range + 1, kh);
     }
     if (ncta > 1)
         cooperative_groups::this_cluster().sync();
@@ -170,45 +256,28 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
         __syncthreads();
     if (rank != 0) return;
 
-    // ---- the cut: the key of the last of the `need` best unforced blocks ----
-    // unforced blocks are [f0, f1); n > K, so there are more than `need` of them
-    const int f0 = a.sink, f1 = n - a.recent;
+    // ---- the cut: the key of the last of the `need` best unforced blocks (there are more than `need`) ----
     int need = K - a.sink - a.recent;
     uint32_t cut = 0xffffffffu;  // taken: keys above `cut`, and the first `need` equal to it
     if (need > 0) {
-        uint32_t kl = 0xffffffffu, kh = 0;
-        for (int j = f0 + tid; j < f1; j += nt) {
-            kl = min(kl, keys[j]);
-            kh = max(kh, keys[j]);
-        }
-        kl = __reduce_min_sync(0xffffffffu, kl);
-        kh = __reduce_max_sync(0xffffffffu, kh);
-        if (lane == 0) {
-            wa[warp] = kl;
-            wb[warp] = kh;
-        }
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int w = 0; w < nw; ++w) {
-            kl = min(kl, wa[w]);
-            kh = max(kh, wb[w]);
-        }
+        kl = misc[0];
+        kh = misc[1];
         for (;;) {
             // bins of 2^sh keys over [kl, kh]
             const int sh = max(0, 24 - __clz((int)(kh - kl)));
-            for (int j = f0 + tid; j < f1; j += nt) {
+            for (int j = f0 + tid; j < f1; j += NT) {
                 const uint32_t k = keys[j];
                 if (k >= kl && k <= kh) atomicAdd(&hist[(k - kl) >> sh], 1u);
             }
             __syncthreads();
             if (warp == 0) {
                 // lane l: bins 255 - 8 l .. 248 - 8 l, from the top
-                uint32_t s[8], sum = 0;
+                const uint4 h1 = reinterpret_cast<const uint4 *>(hist)[63 - 2 * lane],
+                            h0 = reinterpret_cast<const uint4 *>(hist)[62 - 2 * lane];
+                const uint32_t s[8] = {h1.w, h1.z, h1.y, h1.x, h0.w, h0.z, h0.y, h0.x};
+                uint32_t sum = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    s[i] = hist[255 - 8 * lane - i];
-                    sum += s[i];
-                }
+                for (int i = 0; i < 8; ++i) sum += s[i];
                 uint32_t up = sum;  // inclusive over the lanes
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -221,73 +290,100 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         if (acc < (uint32_t)need && acc + s[i] >= (uint32_t)need) {
-                            misc[0] = 255 - 8 * lane - i;  // the bin that holds the cut
-                            misc[1] = acc;                 // keys above it
-                            misc[2] = s[i];
+                            misc[2] = 255 - 8 * lane - i;  // the bin that holds the cut
+                            misc[3] = acc;                 // keys above it
+                            misc[4] = s[i];
                         }
                         acc += s[i];
                     }
                 }
             }
             __syncthreads();
-            const uint32_t bin = misc[0], above = misc[1], in = misc[2];
-            if (tid < 256) hist[tid] = 0;
+            const uint32_t bin = misc[2], above = misc[3], in = misc[4];
             need -= (int)above;
             kl += bin << sh;
-            if (in == (uint32_t)need) {  // the whole bin is taken
-                cut = kl - 1;            // kl > 0: a key of 0 is a block outside the pool, see below
+            if (in == (uint32_t)need && kl > 0) {  // the whole bin is taken
+                cut = kl - 1;
                 need = 0;
-                if (kl == 0) {
-                    cut = 0;
-                    need = 0x7fffffff;
-                }
                 break;
             }
-            if (sh == 0) {
+            if (sh == 0) {  // one key per bin
                 cut = kl;
                 break;
             }
             kh = min(kh, kl + ((1u << sh) - 1));
+            if (in <= S::CAND) {
+                // the bin's keys, ranked against each other
+                for (int j = f0 + tid; j < f1; j += NT) {
+                    const uint32_t k = keys[j];
+                    if (k >= kl && k <= kh) cand[atomicAdd(&misc[5], 1u)] = k;
+                }
+                __syncthreads();
+                for (int i = tid; i < (int)in; i += NT) {
+                    const uint32_t k = cand[i];
+                    int gt = 0, ge = 0;
+                    for (int x = 0; x < (int)in; ++x) {
+                        gt += cand[x] > k;
+                        ge += cand[x] >= k;
+                    }
+                    if (gt < need && need <= ge) {  // equal keys write the same
+                        misc[6] = k;
+                        misc[7] = (uint32_t)(need - gt);
+                    }
+                }
+                __syncthreads();
+                cut = misc[6];
+                need = (int)misc[7];
+                break;
+            }
+            if (tid < 256) hist[tid] = 0;
             __syncthreads();
         }
     }
 
-    // ---- the picks in index order: warp w takes the w-th run of the row ----
-    const int run = ((n + nw - 1) / nw + 31) / 32 * 32, j0 = min(n, warp * run), j1 = min(n, j0 + run);
+    // ---- the picks in index order: every thread a run of the row (of odd length: the lanes' reads
+    // fall into different banks) ----
+    const int run = (n + NT - 1) / NT | 1, r0 = min(n, tid * run), r1 = min(n, r0 + run);
     auto cls = [&](int j) {  // 2: taken, 1: equal to the cut
-        if (j >= j1) return 0;
-        if (j < f0 || j >= f1) return 2;
         const uint32_t k = keys[j];
-        return k > cut ? 2 : k == cut ? 1 : 0;
+        return j < f0 || j >= f1 || k > cut ? 2 : k == cut ? 1 : 0;
     };
     uint32_t gt = 0, eq = 0;
-    for (int j = j0; j < j1; j += 32) {
-        const int k = cls(j + lane);
-        gt += __popc(__ballot_sync(0xffffffffu, k == 2));
-        eq += __popc(__ballot_sync(0xffffffffu, k == 1));
+#pragma unroll 4
+    for (int j = r0; j < r1; ++j) {
+        const int k = cls(j);
+        gt += k == 2;
+        eq += k == 1;
     }
-    __syncthreads();  // wa, wb are read above
-    if (lane == 0) {
-        wa[warp] = gt;
-        wb[warp] = eq;
+    uint32_t gs = gt, es = eq;  // inclusive over the threads
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, gs, o), z = __shfl_up_sync(0xffffffffu, es, o);
+        if (lane >= o) {
+            gs += y;
+            es += z;
+        }
+    }
+    if (lane == 31) {
+        wa[warp] = gs;
+        wb[warp] = es;
     }
     __syncthreads();
-    uint32_t at = 0, eqs = 0;
-    for (int w = 0; w < warp; ++w) {
-        at += wa[w];
-        eqs += wb[w];
-    }
+    uint32_t at = gs - gt, eqs = es - eq;
+#pragma unroll
+    for (int w = 0; w < nw; ++w)
+        if (w < warp) {
+            at += wa[w];
+            eqs += wb[w];
+        }
     at += min(eqs, (uint32_t)need);
-    const uint32_t below = (1u << lane) - 1;
-    for (int j = j0; j < j1; j += 32) {
-        const int k = cls(j + lane);
-        const uint32_t em = __ballot_sync(0xffffffffu, k == 1);
-        const bool take = k == 2 || (k == 1 && eqs + __popc(em & below) < (uint32_t)need);
-        const uint32_t tm = __ballot_sync(0xffffffffu, take);
-        if (take) out[at + __popc(tm & below)] = j + lane;
-        at += __popc(tm);
-        eqs += __popc(em);
-    }
+    if (gt + eq)
+        for (int j = r0; j < r1; ++j) {
+            const int k = cls(j);
+            const bool take = k == 2 || (k == 1 && eqs < (uint32_t)need);
+            if (take) out[at++] = j;
+            eqs += k == 1;
+        }
     if (tid == 0) a.nsel[(size_t)r * a.H + h] = K;
 }
 

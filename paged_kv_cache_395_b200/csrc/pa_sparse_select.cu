@@ -162,31 +162,24 @@ namespace pa {
 
 namespace {
 
-// One cluster per (query row, KV head).
-template <typename T, int D>
-__global__ void __launch_bounds__(512) select_kernel(const SparseArgs a) {
+// One cluster per (query row, KV head).  (256 threads: registers for three CTAs on an SM.)
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(NT, NT == 256 && D <= 128 ? 3 : 1) select_kernel(const SparseArgs a) {
     extern __shared__ __align__(16) unsigned char smem[];
     pdl_wait();
     pdl_release_dependents();
     cg::cluster_group cl = cg::this_cluster();
     const int64_t item = blockIdx.x / cl.num_blocks();
-    select_row<T, D>(a, (int)(item / a.H), (int)(item % a.H), (int)cl.block_rank(), (int)cl.num_blocks(), smem);
+    select_row<T, D, NT>(a, (int)(item / a.H), (int)(item % a.H), (int)cl.block_rank(), (int)cl.num_blocks(), smem);
 }
 
-template <typename T, int D>
-int launch_select_t(const SparseArgs &a, cudaStream_t st) {
-    const int nblk = (a.max_len + kBlockSize - 1) / kBlockSize;
-    const int64_t items = (int64_t)a.rows * a.H;
-    // CTAs per row: enough of them to fill the GPU, each with at least 128 boxes to score
-    int c = 1;
-    while (c < 8 && items * c * 2 <= 2 * 148 && nblk / (2 * c) >= 128) c *= 2;
-    const int threads = nblk / c > 512 ? 512 : 256;
-    const size_t smem = SelectSmem<D>::bytes(a.G, nblk);
-    if (smem > 227 * 1024) return PA_ERR_UNSUPPORTED;
-    if (!set_smem_attr_once(reinterpret_cast<const void *>(select_kernel<T, D>), 227 * 1024)) return PA_ERR_CUDA;
+template <typename T, int D, int NT>
+int launch_select_n(const SparseArgs &a, int c, size_t smem, cudaStream_t st) {
+    auto kern = select_kernel<T, D, NT>;
+    if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), 227 * 1024)) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items * c));
-    cfg.blockDim = dim3(threads);
+    cfg.gridDim = dim3((unsigned)((int64_t)a.rows * a.H * c));
+    cfg.blockDim = dim3(NT);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -197,7 +190,19 @@ int launch_select_t(const SparseArgs &a, cudaStream_t st) {
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, select_kernel<T, D>, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+template <typename T, int D>
+int launch_select_t(const SparseArgs &a, cudaStream_t st) {
+    const int nblk = (a.max_len + kBlockSize - 1) / kBlockSize;
+    const int64_t items = (int64_t)a.rows * a.H;
+    // CTAs per row: enough of them to fill the GPU, each with at least 128 boxes to score
+    int c = 1;
+    while (c < 8 && items * c * 2 <= 2 * 148 && nblk / (2 * c) >= 128) c *= 2;
+    const size_t smem = SelectSmem<D>::bytes(a.G, nblk);
+    if (smem > 227 * 1024) return PA_ERR_UNSUPPORTED;
+    return nblk / c > 512 ? launch_select_n<T, D, 512>(a, c, smem, st) : launch_select_n<T, D, 256>(a, c, smem, st);
 }
 
 template <typename T>
