@@ -50,11 +50,11 @@ __device__ __forceinline__ uint32_t i8_pair(uint32_t u, int b0, int b1) {
     }
 }
 
-// Shared-memory layout of the tensor-core form.
-template <typename T, typename TKV, int D, int NT>
+// Shared-memory layout of the tensor-core form; NWARPS warps per CTA.
+template <typename T, typename TKV, int D, int NT, int NWARPS>
 struct AttendCfg {
     static constexpr bool I8 = std::is_same<TKV, int8_t>::value;
-    static constexpr int NW = 4;                                       // warps
+    static constexpr int NW = NWARPS;
     static constexpr int ROWB = D * (int)sizeof(TKV);                  // bytes per cache row
     static constexpr int SEGB = ROWB < 128 ? ROWB : 128;               // bytes per box row
     static constexpr int TILE = 16 * ROWB;
@@ -72,8 +72,7 @@ struct AttendCfg {
     static constexpr int Q_OFF = RING > JOIN ? RING : JOIN;
     static constexpr int BAR_OFF = Q_OFF + HEADS * QROW;
     static constexpr int INFO_OFF = BAR_OFF + NW * S * 8;              // int [NW][S]: tokens of the stage's block, 0: none
-    static constexpr int SC_OFF = INFO_OFF + NW * S * 4;               // float [NW][S][2]: int8 K, V scales
-    static constexpr int ML_OFF = SC_OFF + NW * S * 8;                 // float [NW][2][HEADS], [2][HEADS], [8][HEADS]
+    static constexpr int ML_OFF = INFO_OFF + NW * S * 4;               // float [NW][2][HEADS], [2][HEADS], [8][HEADS]
     static constexpr int BYTES = 1024 + ML_OFF + (NW * 2 + 10) * HEADS * 4;
     static constexpr bool QREG = NT * D <= 256;                        // q fragments kept in registers
 };
@@ -181,17 +180,16 @@ __device__ __forceinline__ void attend_init(unsigned char *smem) {
 
 // The chosen blocks of row r and KV head h, 8 * NT query heads from 8 * NT * grp on.
 // smem: 1024-byte aligned, AttendCfg bytes, after attend_init.  Called by NW * 32 threads of each CTA.
-template <typename T, typename TKV, int D, int NT>
+template <typename T, typename TKV, int D, int NT, int NWARPS>
 __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CUtensorMap *tmV, int r, int h, int grp,
                            int rank, int ncta, unsigned char *smem) {
-    using C = AttendCfg<T, TKV, D, NT>;
+    using C = AttendCfg<T, TKV, D, NT, NWARPS>;
     constexpr int NW = C::NW, S = C::S, NB = C::NB, KS = D / 16, MT = D / 16;
     constexpr bool SPLIT_P = !std::is_same<T, __half>::value;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
     const uint32_t sb = smem_addr(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF) + warp * S;
     int *info = reinterpret_cast<int *>(smem + C::INFO_OFF) + warp * S;
-    float *scs = reinterpret_cast<float *>(smem + C::SC_OFF) + warp * S * 2;
     const uint32_t ring = sb + warp * S * C::STAGE;
 
     // The first copies wait for a chain of loads: list entry, its table entry.  Neither asks
@@ -202,7 +200,9 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
     const int W = ncta * NW, w = rank * NW + warp;
     // the warp's blocks: lane l of a batch of 32 holds the l-th
     int p_j = -1, p_x = -1, p_y = -1;
-    float p_ks = 0.f, p_vs = 0.f;
+    // int8 scales of the items of the last two batches, asked for with the batch and used when its
+    // blocks are: no copy waits for them
+    float b_ks[2] = {0.f, 0.f}, b_vs[2] = {0.f, 0.f};
     auto load_list = [&](int k) {  // items k .. k + 31
         const int64_t i = (int64_t)(k + lane) * W + w;
         p_j = i < a.K ? __ldcg(sel + i) : -1;
@@ -211,9 +211,7 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
     load_list(0);
     const int ncol = min(C::HEADS, a.G - grp * C::HEADS);
     const size_t row0 = ((size_t)r * a.Hq + (size_t)h * a.G + (size_t)grp * C::HEADS) * D;
-    constexpr int QV = C::HEADS * D / 8 / (NW * 32);  // 16-byte vectors of q per thread
-    static_assert(QV * NW * 32 * 8 == C::HEADS * D || (QV == 0 && C::HEADS * D / 8 <= NW * 32), "q vectors");
-    constexpr int QN = QV ? QV : 1;
+    constexpr int QN = (C::HEADS * D / 8 + NW * 32 - 1) / (NW * 32);  // 16-byte vectors of q per thread
     uint4 qv[QN];
     const bool qvec = ((uintptr_t)a.q & 15) == 0;
     if (qvec) {
@@ -235,8 +233,13 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
             if (p_x >= 0 && (int64_t)p_x < a.N) {
                 p_y = p_x * a.H + h;  // host: num_blocks * H below 2^31
                 if constexpr (C::I8) {
-                    p_ks = __ldg(a.ks + p_y);
-                    p_vs = __ldg(a.vs + p_y);
+                    if (k >> 5 & 1) {
+                        b_ks[1] = __ldg(a.ks + p_y);
+                        b_vs[1] = __ldg(a.vs + p_y);
+                    } else {
+                        b_ks[0] = __ldg(a.ks + p_y);
+                        b_vs[0] = __ldg(a.vs + p_y);
+                    }
                 }
             } else {
                 raise_flag(PA_EFLAG_BAD_BLOCK);
@@ -250,11 +253,6 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
             judge(k);
         }
         const int y = __shfl_sync(0xffffffffu, p_y, k % 32), j = __shfl_sync(0xffffffffu, p_j, k % 32);
-        float ks = 0.f, vs = 0.f;
-        if constexpr (C::I8) {
-            ks = __shfl_sync(0xffffffffu, p_ks, k % 32);
-            vs = __shfl_sync(0xffffffffu, p_vs, k % 32);
-        }
         if (lane == 0) {
             const int s = k % S;
             if (y >= 0) {
@@ -265,10 +263,6 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
                 mbar_arrive(&bars[s]);
             }
             info[s] = y >= 0 ? min(kBlockSize, L - j * kBlockSize) : 0;
-            if constexpr (C::I8) {
-                scs[2 * s] = ks;
-                scs[2 * s + 1] = vs;
-            }
         }
         __syncwarp();
     };
@@ -403,7 +397,9 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
         }
 #pragma unroll
         for (int n1 = 0; n1 < NB; ++n1) {
-            const float sc = C::I8 ? a.scale_log2 * scs[2 * ((k + n1) % S)] : a.scale_log2;
+            float sc = a.scale_log2;
+            if constexpr (C::I8)
+                sc *= __shfl_sync(0xffffffffu, (k + n1) >> 5 & 1 ? b_ks[1] : b_ks[0], (k + n1) & 31);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -518,7 +514,8 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
 #pragma unroll
             for (int n1 = 0; n1 < NB; ++n1) {
                 // a block that is not there: its codes are whatever the stage held, times 0
-                const float vs = valid[n1] > 0 ? scs[2 * ((k + n1) % S) + 1] : 0.f;
+                const float vb = __shfl_sync(0xffffffffu, (k + n1) >> 5 & 1 ? b_vs[1] : b_vs[0], (k + n1) & 31);
+                const float vs = valid[n1] > 0 ? vb : 0.f;
 #pragma unroll
                 for (int sg = 0; sg < MT / MS; ++sg) {
                     uint32_t rw[4][4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9

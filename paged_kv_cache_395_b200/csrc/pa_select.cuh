@@ -166,11 +166,17 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
             float s = __fdiv_rn(m, 127.0f);
             if (!(s < kInf)) s = 0.f;
             if (lane == 0) qs[hd] = s;
+            const float inv = s > 0.f ? __fdividef(1.f, s) : 0.f;
+            // x / s by the reciprocal is off by less than 2^-21 * 127 < 1e-4, so its rounding is the
+            // quotient's unless it lies that near to a half (or the reciprocal is out of range)
+            const bool safe = s > 1e-30f && s < 1e30f;
             uint32_t lo[(EL + 3) / 4] = {}, hi[(EL + 3) / 4] = {};
 #pragma unroll
             for (int e = 0; e < EL; ++e) {
-                int k = 0;
-                if (s > 0.f) k = max(-127, min(127, __float2int_rn(__fdiv_rn(qx[i][e], s))));
+                float y = qx[i][e] * inv;
+                const float f = fabsf(y) - truncf(fabsf(y));
+                if (s > 0.f && (!safe || fabsf(f - 0.5f) < 1e-4f)) y = __fdiv_rn(qx[i][e], s);
+                const int k = s > 0.f ? max(-127, min(127, __float2int_rn(y))) : 0;
                 lo[e / 4] |= (uint32_t)(min(k, 0) & 0xff) << (8 * (e % 4));
                 hi[e / 4] |= (uint32_t)max(k, 0) << (8 * (e % 4));
             }

@@ -202,7 +202,8 @@ int launch_select_t(const SparseArgs &a, cudaStream_t st) {
     while (c < 8 && items * c * 2 <= 2 * 148 && nblk / (2 * c) >= 128) c *= 2;
     const size_t smem = SelectSmem<D>::bytes(a.G, nblk);
     if (smem > 227 * 1024) return PA_ERR_UNSUPPORTED;
-    return nblk / c > 512 ? launch_select_n<T, D, 512>(a, c, smem, st) : launch_select_n<T, D, 256>(a, c, smem, st);
+    // 512 threads where a CTA has many boxes, or few rows leave the SMs to the one that picks
+    return nblk / c > 512 || nblk > 1024 ? launch_select_n<T, D, 512>(a, c, smem, st) : launch_select_n<T, D, 256>(a, c, smem, st);
 }
 
 template <typename T>
