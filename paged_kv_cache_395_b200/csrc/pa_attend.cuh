@@ -610,15 +610,25 @@ __device__ void attend_row_f32(const SparseArgs &a, int r, int h, int grp, int r
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float *os = reinterpret_cast<float *>(smem), *qs = reinterpret_cast<float *>(smem + C::Q_OFF),
           *ml = reinterpret_cast<float *>(smem + C::ML_OFF);
-    int b;
-    const int L = sparse_row_len(a, r, b), nb = (L + kBlockSize - 1) / kBlockSize;
+    // as in attend_row: the list and its table entries wait for no length
     const size_t list = (size_t)r * a.H + h;
-    const int n = min(max(__ldcg(a.nsel + list), 0), a.K);
-    const int32_t *sel = a.sel + list * a.K, *table = a.tables + (size_t)b * a.M;
+    const int32_t *sel = a.sel + list * a.K, *table = a.tables + (size_t)(r / a.Q) * a.M;
+    const int W = ncta * NW, w = rank * NW + warp;
+    int p_j = -1, p_x = -1;
+    auto load_list = [&](int k) {  // items k .. k + 31 of the warp, one per lane
+        const int64_t i = (int64_t)(k + lane) * W + w;
+        p_j = i < a.K ? __ldcg(sel + i) : -1;
+        p_x = p_j >= 0 && p_j < a.M ? __ldcg(table + p_j) : -1;
+    };
+    load_list(0);
     const int ncol = min(GT, a.G - grp * GT);
     const size_t row0 = ((size_t)r * a.Hq + (size_t)h * a.G + (size_t)grp * GT) * D;
     for (int i = tid; i < GT * D; i += NW * 32)
-        qs[i] = i < ncol * D ? reinterpret_cast<const float *>(a.q)[row0 + i] : 0.f;
+        qs[i] = i < ncol * D ? __ldg(reinterpret_cast<const float *>(a.q) + row0 + i) : 0.f;
+    int b;
+    const int L = sparse_row_len(a, r, b), nb = (L + kBlockSize - 1) / kBlockSize;
+    const int n = min(max(__ldcg(a.nsel + list), 0), a.K);
+    const int cnt = n > w ? (n - w + W - 1) / W : 0;
     __syncthreads();
     float o[GT][DL] = {}, m[GT], l[GT];
 #pragma unroll
@@ -627,10 +637,11 @@ __device__ void attend_row_f32(const SparseArgs &a, int r, int h, int grp, int r
         l[t] = 0.f;
     }
     const int tok = lane & 15, half = lane >> 4;
-    for (int i = rank * NW + warp; i < n; i += ncta * NW) {
-        const int j = __ldcg(sel + i);
+    constexpr bool VREG = DL <= 4;  // the 16 rows of V on their way while the scores are made
+    for (int k = 0; k < cnt; ++k) {
+        if (k > 0 && k % 32 == 0) load_list(k);
+        const int j = __shfl_sync(0xffffffffu, p_j, k % 32), x = __shfl_sync(0xffffffffu, p_x, k % 32);
         if (j < 0 || j >= nb) continue;
-        const int x = table[j];
         if (x < 0 || (int64_t)x >= a.N) {
             if (lane == 0) raise_flag(PA_EFLAG_BAD_BLOCK);
             continue;
@@ -638,13 +649,38 @@ __device__ void attend_row_f32(const SparseArgs &a, int r, int h, int grp, int r
         const int valid = min(kBlockSize, L - j * kBlockSize);
         const size_t tile = ((size_t)x * a.H + h) * (kBlockSize * D);
         const float4 *kp = reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(a.kc) + tile + tok * D + half * (D / 2));
-        float s[GT] = {};
+        const float *vp = reinterpret_cast<const float *>(a.vc) + tile + lane * VL;
+        auto vrow = [&](int u, float *v) {
+#pragma unroll
+            for (int e = 0; e < DL; e += VL) {
+                if constexpr (VL == 4) {
+                    const float4 f = __ldg(reinterpret_cast<const float4 *>(vp + u * D + e * 32));
+                    v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
+                } else {
+                    const float2 f = __ldg(reinterpret_cast<const float2 *>(vp + u * D + e * 32));
+                    v[e] = f.x, v[e + 1] = f.y;
+                }
+            }
+        };
+        float s[GT] = {}, v[VREG ? kBlockSize : 1][DL];
+        if constexpr (VREG) {
+#pragma unroll
+            for (int u = 0; u < kBlockSize; ++u) {
+                // rows behind the last token may hold NaN: 0 there
+                if (u < valid) {
+                    vrow(u, v[u]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < DL; ++e) v[u][e] = 0.f;
+                }
+            }
+        }
 #pragma unroll 8
-        for (int v = 0; v < D / 8; ++v) {
-            const float4 k4 = __ldg(kp + v);
+        for (int i = 0; i < D / 8; ++i) {
+            const float4 k4 = __ldg(kp + i);
 #pragma unroll
             for (int t = 0; t < GT; ++t) {
-                const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * D + half * (D / 2) + 4 * v);
+                const float4 q4 = *reinterpret_cast<const float4 *>(qs + t * D + half * (D / 2) + 4 * i);
                 s[t] += k4.x * q4.x + k4.y * q4.y + k4.z * q4.z + k4.w * q4.w;
             }
         }
@@ -663,26 +699,25 @@ __device__ void attend_row_f32(const SparseArgs &a, int r, int h, int grp, int r
 #pragma unroll
             for (int e = 0; e < DL; ++e) o[t][e] *= al;
         }
-        const float *vp = reinterpret_cast<const float *>(a.vc) + tile;
-#pragma unroll 4
-        for (int u = 0; u < valid; ++u) {  // only the tokens that are there: what lies behind may be NaN
-            float v[DL];
+        if constexpr (VREG) {
 #pragma unroll
-            for (int e = 0; e < DL; e += VL) {
-                const float *p = vp + u * D + e * 32 + lane * VL;
-                if constexpr (VL == 4) {
-                    const float4 f = __ldg(reinterpret_cast<const float4 *>(p));
-                    v[e] = f.x, v[e + 1] = f.y, v[e + 2] = f.z, v[e + 3] = f.w;
-                } else {
-                    const float2 f = __ldg(reinterpret_cast<const float2 *>(p));
-                    v[e] = f.x, v[e + 1] = f.y;
+            for (int u = 0; u < kBlockSize; ++u)
+#pragma unroll
+                for (int t = 0; t < GT; ++t) {
+                    const float p = __shfl_sync(0xffffffffu, s[t], u);
+#pragma unroll
+                    for (int e = 0; e < DL; ++e) o[t][e] += p * v[u][e];
                 }
-            }
+        } else {
+#pragma unroll 4
+            for (int u = 0; u < valid; ++u) {  // only the tokens that are there: what lies behind may be NaN
+                vrow(u, v[0]);
 #pragma unroll
-            for (int t = 0; t < GT; ++t) {
-                const float p = __shfl_sync(0xffffffffu, s[t], u);
+                for (int t = 0; t < GT; ++t) {
+                    const float p = __shfl_sync(0xffffffffu, s[t], u);
 #pragma unroll
-                for (int e = 0; e < DL; ++e) o[t][e] += p * v[e];
+                    for (int e = 0; e < DL; ++e) o[t][e] += p * v[0][e];
+                }
             }
         }
     }

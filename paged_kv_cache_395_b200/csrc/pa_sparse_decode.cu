@@ -69,7 +69,7 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), int64_t ctas, int c, int thre
     attr[1].val.clusterDim.x = c;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = c > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 

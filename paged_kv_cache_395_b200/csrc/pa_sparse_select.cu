@@ -189,7 +189,7 @@ int launch_select_n(const SparseArgs &a, int c, size_t smem, cudaStream_t st) {
     attr[1].val.clusterDim.x = c;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = c > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

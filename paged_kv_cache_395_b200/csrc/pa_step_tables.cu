@@ -455,7 +455,7 @@ int launch_step_tables(const StepArgs &a, cudaStream_t st) {
     attr[1].val.clusterDim.x = ncta;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = ncta > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return PA_ERR_CUDA;
     if (few) return PA_OK;
     const size_t smem2 = (size_t)a.B * 8;
