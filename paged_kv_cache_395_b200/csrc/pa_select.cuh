@@ -111,7 +111,7 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
         return;
     }
     const int f0 = a.sink, f1 = n - a.recent;  // the unforced blocks
-    if (tid < 256) hist[tid] = 0;
+    for (int i = tid; i < 256; i += NT) hist[i] = 0;
     if (tid == 0) {
         misc[0] = 0xffffffffu;  // smallest and largest key of the unforced blocks
         misc[1] = 0;
@@ -342,7 +342,7 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
                 need = (int)misc[7];
                 break;
             }
-            if (tid < 256) hist[tid] = 0;
+            for (int i = tid; i < 256; i += NT) hist[i] = 0;
             __syncthreads();
         }
     }
