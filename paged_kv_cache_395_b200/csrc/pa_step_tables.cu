@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
     extern __shared__ unsigned char smem_raw[];
     __shared__ long long ws64[32];
     __shared__ int ws32[32];
-    __shared__ int s_kept, s_claim;  // blocks this CTA pushes; whether it met one that several entries freed
+    __shared__ int2 s_push;  // blocks this CTA pushes; whether it met one that several entries freed
     const Smem s(smem_raw, a.B);
     const int tid = threadIdx.x, nt = blockDim.x, B = a.B, M = a.M, N = a.N, T = a.T;
     cg::cluster_group cl = cg::this_cluster();
@@ -213,12 +213,16 @@ __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
         }
         block_scan(kept, ws32, &all_kept);
         claim = __syncthreads_or(claim);
-        if (tid == 0) {
-            s_kept = all_kept;
-            s_claim = claim;
-        }
-        barrier();
-        for (int r = 0; r < ncta && ncta > 1; ++r) claim |= *cl.map_shared_rank(&s_claim, r) != 0;
+        // lane r of every warp reads CTA r's word
+        const int lane = tid & 31;
+        auto exchange = [&]() -> int2 {
+            if (tid == 0) s_push = make_int2(all_kept, claim);
+            barrier();
+            if (lane >= ncta) return make_int2(0, 0);
+            return ncta > 1 ? *cl.map_shared_rank(&s_push, lane) : s_push;
+        };
+        int2 theirs = exchange();
+        claim = __any_sync(0xffffffffu, theirs.y);
         if (claim) {  // the same in every CTA
             for (int e = f0; e < e1; e += nt) {
                 const int x = entry(e);
@@ -236,15 +240,11 @@ __global__ void __launch_bounds__(1024) step_tables_kernel(const StepArgs a) {
                 if (i < E) k0 |= (uint32_t)k << i;
             }
             block_scan(kept, ws32, &all_kept);
-            if (tid == 0) s_kept = all_kept;
-            barrier();
+            barrier();  // the words of the first exchange are read
+            theirs = exchange();
         }
-        int at = count, pushed = 0;
-        for (int r = 0; r < ncta; ++r) {
-            const int k = ncta > 1 ? *cl.map_shared_rank(&s_kept, r) : all_kept;
-            if (r < rank) at += k;
-            pushed += k;
-        }
+        int at = count + __reduce_add_sync(0xffffffffu, lane < rank ? theirs.x : 0);
+        int pushed = __reduce_add_sync(0xffffffffu, theirs.x);
         auto push = [&](int x, bool k) {  // the next nt entries, in order
             int all;
             const int nth = at + block_scan((int)k, ws32, &all) - 1;
@@ -382,20 +382,30 @@ __global__ void __launch_bounds__(512) step_slots_kernel(const StepArgs a) {
     }
     __syncthreads();
     const int live = (int)min(all, (long long)T);
+    // four tokens per thread and turn, their table entries asked for together
+    constexpr int U = 4;
     int row = 0;
-    for (int t = blockIdx.x * nt + tid; t < T; t += gridDim.x * nt) {
-        long long slot = -1;
-        int p = -1;
-        if (t < live) {
-            row = row_of(start, row, B, t);
-            if (base[row] >= 0) {
-                p = base[row] + t - start[row];
-                const int x = __ldcg(a.tables + (size_t)row * M + p / kBlockSize);
-                slot = x >= 0 && x < N ? (long long)x * kBlockSize + p % kBlockSize : -1;
+    for (int64_t t0 = (int64_t)blockIdx.x * (nt * U) + tid; t0 < T; t0 += (int64_t)gridDim.x * (nt * U)) {
+        int p[U], x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t0 + u * nt;
+            p[u] = x[u] = -1;
+            if (t < live) {
+                row = row_of(start, row, B, (int)t);
+                if (base[row] >= 0) {
+                    p[u] = base[row] + (int)t - start[row];
+                    x[u] = __ldcg(a.tables + (size_t)row * M + p[u] / kBlockSize);
+                }
             }
         }
-        a.slots[t] = slot;
-        if (a.pos) a.pos[t] = p;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t t = t0 + u * nt;
+            if (t >= T) break;
+            a.slots[t] = x[u] >= 0 && x[u] < N ? (long long)x[u] * kBlockSize + p[u] % kBlockSize : -1;
+            if (a.pos) a.pos[t] = p[u];
+        }
     }
 }
 
