@@ -2,12 +2,12 @@
 against the numpy model in 64 bits, the choice of pa_decode_sparse bit for bit, and a
 decode loop of all the step's calls (GPU).
 
-Tolerances (|err| <= atol + rtol |ref|, gpu_util.TOL and its derivation): the fp32 result
-before its rounding to the output type.  fp16 and bf16: products of exact inputs are summed
-in fp32; P is rounded to fp16 (2^-11 of each weight, so at most 2^-11 max|v| < 2.5e-3 / 1 of
-|v| <= 5 in the worst case, and about 2^-11 |v| / sqrt(tokens) on average) or to two bf16
-(2^-17).  A 16-bit output adds half a step of its type: fp16 2^-11 |ref|, inside rtol; bf16
-is checked as an fp32 output and then for being its rounding."""
+Tolerances: |err| <= atol + rtol |ref| of gpu_util.TOL.  fp16: each weight is rounded once
+to 11 bits, so the result moves by at most 2^-11 sum_t w_t |v_t| <= 2^-11 max|v| (2.4e-3 for
+|v| = 5, about 2^-11 |v| / sqrt(tokens) in earnest), and the output's own rounding by 2^-11
+|ref|; bf16: P in two parts (2^-17), its output is checked as fp32 and then for being that
+value's rounding; fp32: sums in fp32, exponentials to 2^-22.
+"""
 import ctypes
 
 import numpy as np
@@ -381,3 +381,141 @@ def test_a_sparse_decode_loop(captured):
             ref = M.attend(qf, kp, vp, t, [n], ws, wc, d ** -0.5, n)[0, 0]
             assert np.all(np.abs(out_h[b] - ref) <= 2e-3 + 2e-3 * np.abs(ref))
     assert pa.pa_get_error_flags(reset=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
+def test_nan_and_infinity_inside_a_row_are_seen(dtype):
+    """A NaN key or value of a token that is there shows in its KV head's rows and nowhere else;
+    its block's box is not finite, so the block is chosen."""
+    w = Case([400, 400, 333], 2, 2, 64, dtype, seed=12)
+    for what in ("k", "v"):
+        kf, vf = w.kf.copy(), w.vf.copy()
+        x = int(w.tables[1, 7])
+        (kf if what == "k" else vf)[x, 1, 3, 5] = np.nan
+        w.dev["kc"], w.dev["vc"] = to_dev(to_store(kf.astype(np.float64), dtype), dtype), \
+            to_dev(to_store(vf.astype(np.float64), dtype), dtype)
+        codes, s = M.boxes(kf)
+        w.dev["bounds"], w.dev["bs"] = to_dev(codes, "i"), to_dev(s, "f")
+        out, sel, cnt = w.sparse(12 if what == "k" else 25, 1, 1, True)
+        got = out.cpu().numpy().reshape(3, 2, 2, 64)
+        bad = np.isnan(got).reshape(3, 2, -1).any(-1)
+        assert bad.tolist() == [[False, False], [False, True], [False, False]], what
+        if what == "k":
+            assert 7 in sel[1, 0, 1] and np.isnan(got[1, 1]).all()
+        else:  # only the value's dim
+            assert np.isnan(got[1, 1, :, 5]).all() and not np.isnan(got[1, 1, :, 6]).any()
+
+
+@pytest.mark.gpu
+def test_pool_past_32_bit_offsets():
+    """Tiles whose elements lie beyond 2^31 and whose bytes beyond 2^32."""
+    H, d, N = 8, 128, 150000          # 2.46e9 elements, 4.9e9 bytes a cache
+    kc = torch.zeros((N, H, BS, d), dtype=torch.float16, device="cuda")
+    vc = torch.zeros_like(kc)
+    lens, n = [300, 77], 19
+    rng = np.random.default_rng(3)
+    t = np.full((2, n), -1, np.int32)
+    ids = N - 1 - rng.permutation(40)[:19 + 5].astype(np.int32)
+    t[0], t[1, :5] = ids[:19], ids[19:]
+    t[0, 3] = 2
+    used = np.unique(t[t >= 0])
+    k, v = rng.standard_normal((len(used), H, BS, d)).astype(np.float16), rng.standard_normal((len(used), H, BS, d)).astype(np.float16)
+    at = torch.from_numpy(used.astype(np.int64)).cuda()
+    # the append writes these slots too
+    slots = (at[:, None] * BS + torch.arange(BS, device="cuda")).reshape(-1)
+    kt = torch.from_numpy(np.ascontiguousarray(k.transpose(0, 2, 1, 3)).reshape(-1, H, d)).cuda()
+    vt = torch.from_numpy(np.ascontiguousarray(v.transpose(0, 2, 1, 3)).reshape(-1, H, d)).cuda()
+    pa.pa_reshape_and_cache(kt, vt, kc, vc, slots)
+    bounds, bs = torch.zeros((N, H, 2, d), dtype=torch.int8, device="cuda"), torch.zeros((N, H), device="cuda")
+    td, ld = torch.from_numpy(t).cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    pa.pa_block_bounds(bounds, bs, kc, td, ld, 300)
+    q = rng.standard_normal((2, H * 2, d)).astype(np.float16)
+    K = 6
+    sel, cnt = torch.zeros((2, H, K), dtype=torch.int32, device="cuda"), torch.zeros((2, H), dtype=torch.int32, device="cuda")
+    out = torch.zeros((2, H * 2, d), dtype=torch.float16, device="cuda")
+    pa.pa_get_error_flags(reset=True)
+    pa.pa_decode_sparse(out, torch.from_numpy(q).cuda(), kc, vc, bounds, bs, td, ld, sel, cnt, d ** -0.5, 304, 1, 2)
+    assert pa.pa_get_error_flags(reset=True) == 0
+    # the model on a small pool of the same tiles
+    where = {int(x): i for i, x in enumerate(used)}
+    small = np.array([[where.get(int(x), -1) for x in row] for row in t], np.int32)
+    kf, vf = k.astype(np.float32), v.astype(np.float32)
+    codes, s = M.boxes(kf)
+    qf = q.astype(np.float32)[:, None]
+    ws, wc = M.choose(qf, codes, s, small, lens, K, 1, 2, 304)
+    assert np.array_equal(sel.cpu().numpy(), ws[:, 0]) and np.array_equal(cnt.cpu().numpy(), wc[:, 0])
+    assert_close(out, M.attend(qf, kf, vf, small, lens, ws, wc, d ** -0.5, 304)[:, 0], "float16")
+
+
+@pytest.mark.gpu
+def test_padded_batch_and_rows_behind():
+    """Rows of length 0 (a padded batch) give zeros, what lies behind the batch stays."""
+    w = Case([200, 0, 64, 0], 2, 4, 128, "float16", seed=3)
+    d = w.dev
+    big = torch.full((6,) + tuple(d["q"].shape[1:]), 7.0, dtype=torch.float16, device="cuda")
+    sel, cnt = torch.full((6, 2, 5), 9, dtype=torch.int32, device="cuda"), torch.full((6, 2), 9, dtype=torch.int32, device="cuda")
+    pa.pa_decode_sparse(big[:4], d["q"], d["kc"], d["vc"], d["bounds"], d["bs"], d["tables"], d["lens"], sel[:4], cnt[:4],
+                        w.scale, w.max_len)
+    assert (big[4:] == 7).all() and (sel[4:] == 9).all() and (cnt[4:] == 9).all()
+    assert (big[[1, 3]] == 0).all() and (sel[[1, 3]] == -1).all() and (cnt[[1, 3]] == 0).all()
+    assert_close(big[:4], w.model(sel[:4, None].cpu().numpy(), cnt[:4, None].cpu().numpy())[:, 0], "float16")
+
+
+@pytest.mark.gpu
+def test_python_refusals():
+    w = Case([100, 50], 2, 4, 64, "float16", seed=1)
+    d = w.dev
+    sel, cnt = torch.zeros((2, 2, 4), dtype=torch.int32, device="cuda"), torch.zeros((2, 2), dtype=torch.int32, device="cuda")
+    out = torch.empty_like(d["q"])
+    good = dict(out=out, q=d["q"], kc=d["kc"], vc=d["vc"], b=d["bounds"], s=d["bs"], t=d["tables"], l=d["lens"], sel=sel,
+                cnt=cnt)
+
+    def call(**kw):
+        a = dict(good, **kw)
+        pa.pa_decode_sparse(a["out"], a["q"], a["kc"], a["vc"], a["b"], a["s"], a["t"], a["l"], a["sel"], a["cnt"],
+                            w.scale, w.max_len)
+
+    call()
+    for bad, message in ((dict(out=out.cpu()), "CUDA"), (dict(l=d["lens"].cpu()), "CUDA"), (dict(b=d["bounds"].cpu()), "CUDA"),
+                         (dict(l=d["lens"].long()), "int32"), (dict(sel=sel.long()), "int32"),
+                         (dict(sel=sel[:, :1]), "selected must"), (dict(cnt=cnt[:1]), "selected must"),
+                         (dict(t=d["tables"][:1]), "block_tables must"), (dict(q=d["q"][:, :, ::2], out=out[:, :, ::2]), "caches|contiguous"),
+                         (dict(t=d["tables"].t().contiguous().t()), "contiguous"), (dict(out=out[:1]), "out must"),
+                         (dict(out=out.bfloat16()), "out must"), (dict(vc=d["vc"].bfloat16()), "caches"),
+                         (dict(vc=d["vc"][:1]), "caches"), (dict(b=d["bounds"].float()), "bounds"),
+                         (dict(b=d["bounds"][:, :, :1]), "bounds"), (dict(s=d["bs"].half()), "bound_scales")):
+        with pytest.raises(ValueError, match=message):
+            call(**bad)
+    with pytest.raises(pa.PaError) as e:
+        pa.pa_decode_sparse(out, d["q"], d["kc"], d["vc"], d["bounds"], d["bs"], d["tables"], d["lens"], sel, cnt, 0.1, 100,
+                            sink_blocks=3, recent_blocks=2)
+    assert e.value.status == pa.PA_ERR_SHAPE
+    with pytest.raises(pa.PaError) as e:
+        pa.pa_decode_selected(out, d["q"], d["kc"].to(torch.int8), d["vc"].to(torch.int8), d["tables"], d["lens"], sel, cnt,
+                              0.1, 100)
+    assert e.value.status == pa.PA_ERR_NULL
+
+
+@pytest.mark.gpu
+def test_two_graphs_and_an_eager_call():
+    """Calls captured without a call before them at these sizes, replayed in turn and beside an
+    eager one."""
+    a, b = Case([777, 1300], 4, 2, 64, "bfloat16", seed=31), Case([3000], 2, 7, 128, "float16", seed=32)
+    graphs, outs = [], []
+    for w, K in ((a, 11), (b, 40)):
+        d = w.dev
+        sel, cnt = torch.zeros(w.lead + (w.H, K), dtype=torch.int32, device="cuda"), torch.zeros(w.lead + (w.H,), dtype=torch.int32, device="cuda")
+        out = torch.zeros_like(d["q"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            pa.pa_decode_sparse(out, d["q"], d["kc"], d["vc"], d["bounds"], d["bs"], d["tables"], d["lens"], sel, cnt, w.scale,
+                                w.max_len, 1, 2)
+        graphs.append(g)
+        outs.append(out)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+        eager = a.sparse(11, 1, 2)[0]
+    torch.cuda.synchronize()
+    assert np.array_equal(bits(outs[0]), bits(eager)) and np.array_equal(bits(outs[1]), bits(b.sparse(40, 1, 2)[0]))
