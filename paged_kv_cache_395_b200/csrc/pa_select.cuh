@@ -354,12 +354,15 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
         const uint32_t k = keys[j];
         return j < f0 || j >= f1 || k > cut ? 2 : k == cut ? 1 : 0;
     };
-    uint32_t gt = 0, eq = 0;
+    // of the run: how many, and (up to 32 blocks) which
+    uint32_t gt = 0, eq = 0, gm = 0, em = 0;
 #pragma unroll 4
     for (int j = r0; j < r1; ++j) {
         const int k = cls(j);
         gt += k == 2;
         eq += k == 1;
+        gm |= (uint32_t)(k == 2) << ((j - r0) & 31);
+        em |= (uint32_t)(k == 1) << ((j - r0) & 31);
     }
     uint32_t gs = gt, es = eq;  // inclusive over the threads
 #pragma unroll
@@ -383,13 +386,17 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
             eqs += wb[w];
         }
     at += min(eqs, (uint32_t)need);
-    if (gt + eq)
+    if (run <= 32) {
+        for (uint32_t all = gm | em; all; all &= all - 1) {
+            const uint32_t bit = all & -all;
+            if ((gm & bit) || eqs++ < (uint32_t)need) out[at++] = r0 + __ffs(bit) - 1;
+        }
+    } else if (gt + eq) {
         for (int j = r0; j < r1; ++j) {
             const int k = cls(j);
-            const bool take = k == 2 || (k == 1 && eqs < (uint32_t)need);
-            if (take) out[at++] = j;
-            eqs += k == 1;
+            if (k == 2 || (k == 1 && eqs++ < (uint32_t)need)) out[at++] = j;
         }
+    }
     if (tid == 0) a.nsel[(size_t)r * a.H + h] = K;
 }
 
