@@ -264,16 +264,20 @@ template <typename T, int D>
 int launch_select_t(const SparseArgs &a, cudaStream_t st) {
     const int nblk = (a.max_len + kBlockSize - 1) / kBlockSize;
     const int64_t items = (int64_t)a.rows * a.H;
-    // CTAs per row: enough of them to fill the GPU, each with at least 128 boxes to score
-    int c = 1;
-    while (c < 8 && items * c * 2 <= 2 * 148 && nblk / (2 * c) >= 128) c *= 2;
+    // CTAs per row: as many as give every SM one, each with at least 128 boxes to score
+    int c = (int)(items < 148 ? 148 / items : 1);
+    if (c > 8) c = 8;
+    while (c > 1 && nblk / c < 128) --c;
     const size_t smem = SelectSmem<D>::bytes(a.G, nblk);
     if (smem > 227 * 1024) return PA_ERR_UNSUPPORTED;
-    // 512 threads where a CTA has many boxes, or few rows leave the SMs to the one that picks; 128
-    // for very many short rows, whose picking is then spread over more CTAs (1024 rows 18.9 -> 15 us;
-    // 512 rows, of which half need no choice, 7.9 with 256 threads, 9.9 with 128)
+    // Threads: 512 where the SMs have a CTA each at most, with more than a tile for each of 8 warps
+    // (128 rows of 256 blocks 5.8 us, with two CTAs of 256 threads a row 7.0; of 512 blocks 7.1 against
+    // 9.1), or where a CTA's boxes are many; 128 for very many short rows, whose picking is then
+    // spread over more CTAs (1024 rows 15 us, with 256 threads 18.9; but 512 rows, of which half need
+    // no choice, 9.9 against 7.9).
     if (items > 6 * 148 && nblk <= 512) return launch_select_n<T, D, 128>(a, c, smem, st);
-    return nblk / c > 512 || nblk > 1024 ? launch_select_n<T, D, 512>(a, c, smem, st) : launch_select_n<T, D, 256>(a, c, smem, st);
+    if ((items * c <= 148 && nblk / c > 128) || nblk / c > 512) return launch_select_n<T, D, 512>(a, c, smem, st);
+    return launch_select_n<T, D, 256>(a, c, smem, st);
 }
 
 template <typename T>
