@@ -565,10 +565,16 @@ def _list_rules(q, H, block_tables, seq_lens, selected, num_selected):
 
 def _lists_good(q, shape, H, dev, block_tables, seq_lens, selected, num_selected):
     """What the block-sparse calls ask of q (of that shape), the lists, tables and lengths."""
-    lead = shape[:-2]
-    return (dev >= 0 and dev == _get_device() and 3 <= len(shape) <= 4 and
-            selected.shape[:-1] == lead + (H,) and num_selected.shape == lead + (H,) and
-            block_tables.dim() == 2 and len(block_tables) == shape[0] and seq_lens.numel() == shape[0] and
+    if dev < 0 or dev != _get_device():
+        return False
+    n, listed, B = len(shape), selected.shape, shape[0]
+    if n == 3:
+        if len(listed) != 3 or listed[0] != B or listed[1] != H or num_selected.shape != (B, H):
+            return False
+    elif n != 4 or len(listed) != 4 or listed[:3] != (B, shape[1], H) or num_selected.shape != (B, shape[1], H):
+        return False
+    t = block_tables.shape
+    return (len(t) == 2 and t[0] == B and seq_lens.numel() == B and
             selected.dtype is _I32 and num_selected.dtype is _I32 and block_tables.dtype is _I32 and
             seq_lens.dtype is _I32 and q.is_contiguous() and selected.is_contiguous() and
             num_selected.is_contiguous() and block_tables.is_contiguous() and seq_lens.is_contiguous() and
@@ -609,9 +615,10 @@ def _sparse_decode_params(out, q, key_cache, value_cache, block_tables, seq_lens
     if not (_lists_good(q, shape, H, dev, block_tables, seq_lens, selected, num_selected) and
             value_cache.shape == kshape and value_cache.dtype is key_cache.dtype and bs == BLOCK_SIZE and
             shape[-1] == d and out.shape == shape and (not f32 or out.dtype is _F32) and
-            (k_scales is None or (k_scales.dtype is _F32 and k_scales.shape == (N, H))) and
-            (v_scales is None or (v_scales.dtype is _F32 and v_scales.shape == (N, H))) and
-            _on(dev, out, key_cache, value_cache, k_scales, v_scales)):
+            out.is_contiguous() and key_cache.is_contiguous() and value_cache.is_contiguous() and
+            out.get_device() == key_cache.get_device() == value_cache.get_device() == dev and
+            (k_scales is None or (k_scales.dtype is _F32 and k_scales.shape == (N, H) and _on(dev, k_scales))) and
+            (v_scales is None or (v_scales.dtype is _F32 and v_scales.shape == (N, H) and _on(dev, v_scales)))):
         _refuse([out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected, k_scales, v_scales],
                 _list_rules(q, H, block_tables, seq_lens, selected, num_selected) +
                 [(value_cache.shape != kshape or value_cache.dtype != key_cache.dtype or bs != BLOCK_SIZE or

@@ -248,6 +248,22 @@ def test_choices_of_long_rows(L, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,L", [(10, 16 * 1100), (14, 16 * 900), (20, 16 * 390 + 3), (37, 16 * 300), (50, 16 * 300),
+                                 (74, 16 * 520)])
+def test_choices_at_every_cluster_size(B, L):
+    """Two KV heads and B rows: seven, five, three, two and one CTAs per row, of 256 and 512 threads."""
+    rng = np.random.default_rng(B)
+    H, G, d, n, N, K = 2, 2, 64, -(-L // BS), 300, 30
+    tables = rng.integers(0, N, (B, n)).astype(np.int32)
+    codes, scales = M.boxes(rng.standard_normal((N, H, BS, d)).astype(np.float32))
+    lens = [L - 16 * int(x) for x in rng.integers(0, 40, B)]
+    q = to_store(rng.standard_normal((B, 1, H * G, d)), "bfloat16")
+    got = run_select(q, "bfloat16", codes, scales, tables, lens, K, 1, 2, L)
+    want = M.choose(M.values(q), codes, scales, tables, lens, K, 1, 2, L)
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("Q", [2, 3])
 def test_choices_of_several_new_tokens(Q):
     rng = np.random.default_rng(Q)
