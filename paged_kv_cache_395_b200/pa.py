@@ -485,10 +485,13 @@ def pa_step_tables(block_tables, seq_lens, new_lens, free_blocks, free_count, sl
     B, M = block_tables.shape
     N, T = free_blocks.numel(), slot_mapping.numel()
     dev = block_tables.get_device()
-    good = dev >= 0 and dev == _get_device() and slot_mapping.dtype is _I64 and slot_mapping.get_device() == dev and \
-        slot_mapping.is_contiguous() and block_tables.dtype is _I32 and block_tables.is_contiguous()
-    for t, n in ((seq_lens, B), (new_lens, B), (lens_out, B), (free_blocks, N), (free_count, 1), (count_out, 1),
-                 (positions, T), (row_starts, B + 1), (refcounts, N)):
+    good = (dev >= 0 and dev == _get_device() and slot_mapping.dtype is _I64 and
+            block_tables.dtype is seq_lens.dtype is new_lens.dtype is free_blocks.dtype is free_count.dtype is _I32 and
+            seq_lens.numel() == new_lens.numel() == B and free_count.numel() == 1 and
+            seq_lens.get_device() == new_lens.get_device() == free_blocks.get_device() == free_count.get_device() ==
+            slot_mapping.get_device() == dev and block_tables.is_contiguous() and seq_lens.is_contiguous() and
+            new_lens.is_contiguous() and free_blocks.is_contiguous() and slot_mapping.is_contiguous())
+    for t, n in ((seq_lens_out, B), (free_count_out, 1), (positions, T), (row_starts, B + 1), (refcounts, N)):
         if t is not None and (t.numel() != n or t.dtype is not _I32 or t.get_device() != dev or not t.is_contiguous()):
             good = False
     if not good:
