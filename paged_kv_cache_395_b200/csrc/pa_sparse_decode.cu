@@ -99,6 +99,15 @@ int launch_attend_t(SparseArgs a, cudaStream_t st) {
     // against 44.9, 1024 rows 80.8 against 84.8 with their choice; 8 rows 16.7 against 15.6).
     if constexpr (NT == 1 && !C::I8 && D <= 128 && NW == 4)
         if ((int64_t)a.rows * a.H >= 3 * 148) return launch_attend_t<T, TKV, D, NT, 3>(a, st);
+    // About a row per SM: one CTA with as many warps as the registers and shared memory hold, instead
+    // of a cluster of smaller ones that have to join their shares (128 int8 rows of 128 blocks 19.1 us
+    // against 19.8 with three CTAs of four warps; 128 rows of 32 heads 27.8 against 29.2 with their
+    // choice; with fewer rows, in clusters, it is the slower form: 15.5 against 14.8 for 8 rows).
+    constexpr int WIDE = NT == 1 ? 12 : 8;
+    if constexpr (D <= 128 && NW == 4) {
+        const int64_t items = (int64_t)a.rows * a.H * ((a.G + C::HEADS - 1) / C::HEADS);
+        if (items <= 148 && 2 * items > 148 && a.K >= 2 * WIDE) return launch_attend_t<T, TKV, D, NT, WIDE>(a, st);
+    }
     a.ng = (a.G + C::HEADS - 1) / C::HEADS;
     const int64_t items = (int64_t)a.rows * a.H * a.ng;
     auto kern = attend_kernel<T, TKV, D, NT, NW>;

@@ -169,6 +169,19 @@ def test_rows_split_over_ctas(dtype, cache, B, L, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("bfloat16", None), ("float32", None), ("float16", "int8"),
+                                         ("bfloat16", "int8")])
+@pytest.mark.parametrize("B,H,G,d", [(50, 2, 4, 128), (50, 2, 4, 64), (90, 1, 16, 128), (100, 1, 32, 64), (90, 1, 20, 128),
+                                     (250, 2, 3, 64)])
+def test_about_a_row_per_sm_and_many_rows(dtype, cache, B, H, G, d):
+    """CTAs of 8 and 12 warps, one per row; many rows in CTAs of 3 or 4."""
+    rng = np.random.default_rng(B)
+    w = Case([int(x) for x in rng.integers(1, 700, B)], H, G, d, dtype, cache, seed=B + d)
+    sel, cnt = w.lists(25, 1)
+    w.check(w.attend(sel, cnt), w.model(sel, cnt), w.attend(sel, cnt, True))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16", "float32"])
 @pytest.mark.parametrize("Q", [2, 3])
 def test_several_new_tokens(dtype, Q):
