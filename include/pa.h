@@ -497,7 +497,7 @@ int pa_step_tables(int32_t *block_tables, const int32_t *seq_lens, const int32_t
  * 0 (pa_select_blocks then prefers it, so that what dense attention would show is seen).
  * An int8 cache's keys are q8 * k_scale.  A block in several tables is written the same
  * by each.  The box of a partly filled block is not needed: a row's newest block is always
- * picked.
+ * picked.  A full block whose keys are written anew (by pa_block_copy, say) needs its box again.
  * Covered are at most ceil(max_new_tokens / 16) blocks per sequence; a sequence that grew
  * by more sets PA_EFLAG_BAD_LENGTH.  Lengths above 16 * max_blocks_per_seq are cut to it.
  * Table entries outside the pool set PA_EFLAG_BAD_BLOCK and are skipped.

@@ -72,21 +72,20 @@ struct AttendCfg {
     static constexpr int Q_OFF = RING > JOIN ? RING : JOIN;
     static constexpr int BAR_OFF = Q_OFF + HEADS * QROW;
     static constexpr int INFO_OFF = BAR_OFF + NW * S * 8;              // int [NW][S]: tokens of the stage's block, 0: none
-    static constexpr int ML_OFF = INFO_OFF + NW * S * 4;               // float [NW][2][HEADS], [2][HEADS], [8][HEADS]
-    static constexpr int BYTES = 1024 + ML_OFF + (NW * 2 + 10) * HEADS * 4;
+    static constexpr int ML_OFF = INFO_OFF + NW * S * 4;               // float [NW][2][HEADS], then [2][HEADS]
+    static constexpr int BYTES = 1024 + ML_OFF + (NW + 1) * 2 * HEADS * 4;
     static constexpr bool QREG = NT * D <= 256;                        // q fragments kept in registers
 };
 
 // Joins the warps' and the CTAs' shares and writes the output.  o: float [NW][HEADS][OROW] shares of
-// the CTA's warps; ml: float [NW][2][HEADS] their maxima and sums, then [2][HEADS] for the CTA's own
-// and [8][HEADS] for the weights of the cluster's CTAs.
+// the CTA's warps; ml: float [NW][2][HEADS] their maxima and sums, then [2][HEADS] for the CTA's own.
 template <typename T, int D, int HEADS, int OROW, int NW>
 __device__ __forceinline__ void join_shares(const SparseArgs &a, float *o, float *ml, int ncol, size_t out0, int rank,
                                             int ncta) {
     constexpr int Q4 = D / 4;  // vectors of four per head
     const int tid = threadIdx.x, nt = NW * 32;
     const float kNegInf = __int_as_float(0xff800000);
-    float *mine = ml + NW * 2 * HEADS, *fr = mine + 2 * HEADS;
+    float *mine = ml + NW * 2 * HEADS;
     __syncthreads();
     if (tid < HEADS) {
         float M = kNegInf, l = 0.f;
@@ -129,43 +128,37 @@ __device__ __forceinline__ void join_shares(const SparseArgs &a, float *o, float
     if (ncta == 1) return;
     cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
     cl.sync();
-    if (tid < HEADS) {
-        float m[8], l[8], M = kNegInf, sum = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            m[r] = r < ncta ? *cl.map_shared_rank(mine + tid, r) : kNegInf;
-            l[r] = r < ncta ? *cl.map_shared_rank(mine + HEADS + tid, r) : 0.f;
-            M = fmaxf(M, m[r]);
-        }
-        if (M == kNegInf) M = 0.f;
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            m[r] = fast_exp2(m[r] - M);
-            sum += m[r] * l[r];
-        }
-        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
-#pragma unroll
-        for (int r = 0; r < 8; ++r) fr[r * HEADS + tid] = m[r] * inv;
-    }
-    __syncthreads();
-    // the CTAs take turns at the row's vectors
+    // the CTAs take turns at the row's vectors; a vector's shares, maxima and sums are read together
     for (int i = rank * nt + tid; i < ncol * Q4; i += ncta * nt) {
         const int g = i / Q4, d = i % Q4 * 4;
         float4 v[8], s = make_float4(0.f, 0.f, 0.f, 0.f);
+        float m[8], l[8], M = kNegInf, sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-            if (r < ncta) v[r] = *cl.map_shared_rank(reinterpret_cast<float4 *>(o + g * OROW + d), r);
+        for (int r = 0; r < 8; ++r) {
+            m[r] = kNegInf;
+            l[r] = 0.f;
+            if (r < ncta) {
+                m[r] = *cl.map_shared_rank(mine + g, r);
+                l[r] = *cl.map_shared_rank(mine + HEADS + g, r);
+                v[r] = *cl.map_shared_rank(reinterpret_cast<float4 *>(o + g * OROW + d), r);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) M = fmaxf(M, m[r]);
+        if (M == kNegInf) M = 0.f;
 #pragma unroll
         for (int r = 0; r < 8; ++r)
             if (r < ncta) {
-                const float f = fr[r * HEADS + g];
+                const float f = fast_exp2(m[r] - M);
+                sum += f * l[r];
                 s.x += f * v[r].x;
                 s.y += f * v[r].y;
                 s.z += f * v[r].z;
                 s.w += f * v[r].w;
             }
-        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, s.x, s.y);
-        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d + 2, s.z, s.w);
+        const float inv = sum == 0.f ? 0.f : __fdividef(1.f, sum);
+        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d, s.x * inv, s.y * inv);
+        store_out2<T>(a.out, a.out_f32, out0 + (size_t)g * D + d + 2, s.z * inv, s.w * inv);
     }
     cl.sync();  // no CTA ends while another reads its shares
 }
@@ -600,7 +593,7 @@ struct AttendF32Cfg {
     static constexpr int NW = 4, OROW = D + 4;
     static constexpr int Q_OFF = NW * GT * OROW * 4;
     static constexpr int ML_OFF = Q_OFF + GT * D * 4;
-    static constexpr int BYTES = ML_OFF + (NW * 2 + 10) * GT * 4;
+    static constexpr int BYTES = ML_OFF + (NW + 1) * 2 * GT * 4;
 };
 
 template <int D, int GT>

@@ -41,8 +41,8 @@ struct SelectSmem {
     static constexpr int QROW = 2 * D + 64;
     static constexpr int CAND = 512;  // keys of the cut's bin that are ranked directly
     static constexpr int MISC = 4 * (256 + CAND + 2 * 32 + 16);
-    static __host__ __device__ int heads(int G) { return (G + 7) / 8 * 8; }
-    static __host__ __device__ size_t bytes(int G, int nblk) {
+    static constexpr __host__ __device__ int heads(int G) { return (G + 7) / 8 * 8; }
+    static constexpr __host__ __device__ size_t bytes(int G, int nblk) {
         return (size_t)heads(G) * (QROW + 4) + MISC + (size_t)((nblk + 31) / 32 * 32) * 4;
     }
 };

@@ -269,7 +269,7 @@ int launch_select_t(const SparseArgs &a, cudaStream_t st) {
     if (c > 8) c = 8;
     while (c > 1 && nblk / c < 128) --c;
     const size_t smem = SelectSmem<D>::bytes(a.G, nblk);
-    if (smem > 227 * 1024) return PA_ERR_UNSUPPORTED;
+    static_assert(SelectSmem<D>::bytes(64, PA_SPARSE_MAX_SEQ_LEN / kBlockSize) <= 227 * 1024, "keys of the longest row");
     // Threads: 512 where the SMs have a CTA each at most, with more than a tile for each of 8 warps
     // (128 rows of 256 blocks 5.8 us, with two CTAs of 256 threads a row 7.0; of 512 blocks 7.1 against
     // 9.1), or where a CTA's boxes are many; 128 for very many short rows, whose picking is then

@@ -268,6 +268,8 @@ def test_empty_batch_and_no_slots():
     z = np.zeros(0, np.int32)
     got = run_kernel(e, z, z, np.arange(8, dtype=np.int32), 5, 6)
     assert got[3][0] == 5 and (got[5] == -1).all() and (got[6] == -1).all() and got[7].tolist() == [0]
+    got = run_kernel(e, z, z, np.arange(8, dtype=np.int32), 5, 9000)
+    assert got[3][0] == 5 and (got[5] == -1).all() and (got[6] == -1).all() and got[7].tolist() == [0]
     check(np.array([[3, 4]], np.int32), np.array([20], np.int32), np.array([-1], np.int32),
           np.array([0, 1, 2, 0, 0], np.int32), 3, 0)
 
