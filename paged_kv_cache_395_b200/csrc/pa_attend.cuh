@@ -163,6 +163,503 @@ __device__ __forceinline__ void join_shares(const SparseArgs &a, float *o, float
     cl.sync();  // no CTA ends while another reads its shares
 }
 
+// Zeroes the V rows behind the last token of a step's blocks: a weight of 0 does not make a NaN
+// there 0.
+template <typename C, int NB>
+__device__ __forceinline__ void zero_rows_past(const uint32_t (&vt)[NB], const int (&valid)[NB], int lane) {
+#pragma unroll
+    for (int n1 = 0; n1 < NB; ++n1)
+        for (int i = lane; i < (kBlockSize - valid[n1]) * (C::ROWB / 16); i += 32) {
+            const int row = valid[n1] + i / (C::ROWB / 16), ch = i % (C::ROWB / 16);
+            asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(swz(vt[n1] + (ch >> 3) * 2048, row, ch & 7)), "r"(0)
+                         : "memory");
+        }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// The streaming part of attend_row with the tokens on the MMA's M side, for up to 8 heads per n-tile
+// and for int8 caches:
+//   S^T[16 tokens x heads] = K[16 x D] . Q^T[D x heads]     (A = K tile, B = q)
+//   O^T[D x heads]        += V^T[D x 16] . P^T[16 x heads]  (A = V tile^T, B = p)
+// arrived(k, ...): waits for blocks k .. k + NB - 1 of the warp; issue(k): requests block k.
+// ks, vs8: the int8 scales of the last two batches of 32 blocks, a block per lane.
+template <typename T, typename TKV, int D, int NT, int NWARPS, typename Arrived, typename Issue>
+__device__ __forceinline__ void stream_tokens_m(const SparseArgs &a, unsigned char *smem, int cnt, const float (&ks)[2],
+                                                const float (&vs8)[2], Arrived arrived, Issue issue) {
+    using C = AttendCfg<T, TKV, D, NT, NWARPS>;
+    constexpr int S = C::S, NB = C::NB, KS = D / 16, MT = D / 16;
+    constexpr bool SPLIT_P = !std::is_same<T, __half>::value;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const uint32_t sb = smem_addr(smem);
+    // B fragments of k-steps ks (and, 16-bit caches, ks + 1) of n-tile t, the dims in the order of
+    // the K fragments
+    auto qfrag = [&](int t, int ks, uint32_t (&f)[4]) {
+        if constexpr (!C::I8) {
+            ldsm_x4(f, sb + C::Q_OFF + (t * 8 + (lane & 7)) * C::QROW + ks * 32 + (lane >> 3) * 16);
+        } else {
+            // thread column c reads 32 (D = 64: 16) contiguous bytes per 128-byte segment of a row
+            const int d0 = D == 64 ? c * 16 + ks * 4 : (ks / 8) * 128 + c * 32 + (ks % 8) * 4;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                         : "r"(sb + C::Q_OFF + (t * 8 + g) * C::QROW + d0 * 2)
+                         : "memory");
+        }
+    };
+    uint32_t qb[C::QREG ? NT : 1][C::QREG ? KS / 2 : 1][4];
+    if constexpr (C::QREG) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int ks = 0; ks < KS; ks += 2) qfrag(t, ks, qb[t][ks / 2]);
+    }
+
+    float o[NT][MT][4] = {};
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        m[t][0] = m[t][1] = __int_as_float(0xff800000);
+        l[t][0] = l[t][1] = 0.f;
+    }
+
+    for (int k = 0; k < cnt; k += NB) {
+        int valid[NB];
+        uint32_t kt[NB], vt[NB];
+        bool whole;
+        if (!arrived(k, valid, kt, vt, whole)) break;
+        // ---- S^T ----
+        float x[NB][NT][4];
+#pragma unroll
+        for (int n1 = 0; n1 < NB; ++n1)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n1][t][e] = 0.f;
+#pragma unroll
+        for (int k2 = 0; k2 < KS; k2 += 2) {
+            uint32_t qf[C::QREG ? 1 : NT][4];
+            if constexpr (!C::QREG) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t) qfrag(t, k2, qf[t]);
+            }
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+                uint32_t af[2][4];
+                if constexpr (!C::I8) {
+                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int ch = (k2 + u) * 2 + (lane >> 4);
+                        ldsm_x4(af[u], swz(kt[n1] + (ch >> 3) * 2048, row, ch & 7));
+                    }
+                } else {
+                    // 8 bytes of tokens g and g + 8
+                    uint32_t wa[2], wb[2];
+                    uint32_t pa, pb;
+                    if constexpr (D == 64) {
+                        pa = kt[n1] + g * 64 + c * 16 + k2 * 4;
+                        pb = pa + 8 * 64;
+                    } else {
+                        const uint32_t seg = kt[n1] + (k2 / 8) * 2048;
+                        pa = swz(seg, g, 2 * c + (k2 % 8) / 4) + (k2 % 4) * 4;
+                        pb = swz(seg, g + 8, 2 * c + (k2 % 8) / 4) + (k2 % 4) * 4;
+                    }
+                    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(wa[0]), "=r"(wa[1]) : "r"(pa) : "memory");
+                    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(wb[0]), "=r"(wb[1]) : "r"(pb) : "memory");
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const uint32_t ua = wa[u] ^ 0x80808080u, ub = wb[u] ^ 0x80808080u;
+                        af[u][0] = i8_pair<T>(ua, 0, 1);
+                        af[u][1] = i8_pair<T>(ub, 0, 1);
+                        af[u][2] = i8_pair<T>(ua, 2, 3);
+                        af[u][3] = i8_pair<T>(ub, 2, 3);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        const uint32_t *f = C::QREG ? qb[t][k2 / 2] : qf[t];
+                        Mma<T>::mma(x[n1][t], af[u], f[2 * u], f[2 * u + 1]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int n1 = 0; n1 < NB; ++n1) {
+            float sc = a.scale_log2;
+            if constexpr (C::I8)
+                sc *= __shfl_sync(0xffffffffu, (k + n1) >> 5 & 1 ? ks[1] : ks[0], (k + n1) & 31);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n1][t][e] *= sc;
+        }
+        if (!whole) {  // rows past the last token hold anything, NaN among it
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (g + 8 * (e >> 1) >= valid[n1]) x[n1][t][e] = __int_as_float(0xff800000);
+        }
+        // ---- running maximum and sum; P ----
+        // The reference of the exponentials follows the maximum only when that grew by more than
+        // 2^8: weights of up to 2^8 are as exact, and the output is seldom rescaled.
+        uint32_t ph[NB][NT][2], pl[SPLIT_P ? NB : 1][SPLIT_P ? NT : 1][2];
+        float mx[NT][2];
+        bool grew = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float v = fmaxf(x[0][t][e], x[0][t][2 + e]);
+                if constexpr (NB > 1) v = fmaxf(v, fmaxf(x[1][t][e], x[1][t][2 + e]));
+                mx[t][e] = v;
+            }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mx[t][e] = fmaxf(mx[t][e], __shfl_xor_sync(0xffffffffu, mx[t][e], d));
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) grew |= mx[t][e] > m[t][e] + 8.f;
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float al[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float mn = mx[t][e] > m[t][e] + 8.f ? mx[t][e] : m[t][e];
+                    al[e] = m[t][e] == mn ? 1.f : fast_exp2(m[t][e] - mn);
+                    m[t][e] = mn;
+                    l[t][e] *= al[e];
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][i][e] *= al[e & 1];
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float mu[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) mu[e] = m[t][e] == __int_as_float(0xff800000) ? 0.f : m[t][e];
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[n1][t][e] = fast_exp2(x[n1][t][e] - mu[e & 1]);
+                    l[t][e & 1] += x[n1][t][e];
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {  // tokens g (e = 0) and g + 8, heads 2c, 2c + 1
+                    const uint32_t hi = Mma<T>::pack(x[n1][t][2 * e], x[n1][t][2 * e + 1]);
+                    ph[n1][t][e] = movm_t(hi);
+                    if constexpr (SPLIT_P) {
+                        const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
+                        pl[n1][t][e] = movm_t(Mma<T>::pack(x[n1][t][2 * e] - h0, x[n1][t][2 * e + 1] - h1));
+                    }
+                }
+            }
+        }
+        // ---- O^T ----
+        if constexpr (!C::I8) {
+            if (!whole) zero_rows_past<C, NB>(vt, valid, lane);
+            const int row = (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const int ch = i * 2 + ((lane >> 3) & 1);
+#pragma unroll
+                for (int n1 = 0; n1 < NB; ++n1) {
+                    uint32_t af[4];
+                    ldsm_x4_t(af, swz(vt[n1] + (ch >> 3) * 2048, row, ch & 7));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        Mma<T>::mma(o[t][i], af, ph[n1][t][0], ph[n1][t][1]);
+                        if constexpr (SPLIT_P) Mma<T>::mma(o[t][i], af, pl[n1][t][0], pl[n1][t][1]);
+                    }
+                }
+            }
+        } else {
+            constexpr int MS = D == 64 ? 4 : 8, VW = D == 64 ? 2 : 4;  // m-tiles and words per segment
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+                // a block that is not there: its codes are whatever the stage held, times 0
+                const float vb = __shfl_sync(0xffffffffu, (k + n1) >> 5 & 1 ? vs8[1] : vs8[0], (k + n1) & 31);
+                const float vs = valid[n1] > 0 ? vb : 0.f;
+#pragma unroll
+                for (int sg = 0; sg < MT / MS; ++sg) {
+                    uint32_t rw[4][4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int row = 2 * c + (q & 1) + 8 * (q >> 1);
+                        if constexpr (D == 64) {
+                            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
+                                         : "=r"(rw[q][0]), "=r"(rw[q][1])
+                                         : "r"(vt[n1] + row * 64 + g * 8)
+                                         : "memory");
+                        } else {
+                            lds_v4(rw[q], swz(vt[n1] + sg * 2048, row, g));
+                        }
+#pragma unroll
+                        for (int e = 0; e < VW; ++e) rw[q][e] ^= 0x80808080u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < MS; ++i) {
+                        uint32_t af[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {  // token pair q / 2, dims row (q & 1 ? g + 8 : g)
+                            const int p = q >> 1, wd = (q & 1) * (VW / 2) + i / 4;
+                            const uint32_t sl = (uint32_t)(i & 3) | (uint32_t)(4 + (i & 3)) << 4;
+                            af[q] = i8_pair<T>(__byte_perm(rw[2 * p][wd], rw[2 * p + 1][wd], sl), 0, 1);
+                        }
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            float d[4];
+                            Mma<T>::mma0(d, af, ph[n1][t][0], ph[n1][t][1]);
+                            if constexpr (SPLIT_P) Mma<T>::mma(d, af, pl[n1][t][0], pl[n1][t][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[t][sg * MS + i][e] += vs * d[e];
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int n1 = 0; n1 < NB; ++n1) issue(k + S + n1);
+    }
+
+    // ---- this warp's share, for the joining ----
+    float *os = reinterpret_cast<float *>(smem);
+    float *ml = reinterpret_cast<float *>(smem + C::ML_OFF);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
+            if (g == 0) {
+                ml[warp * 2 * C::HEADS + t * 8 + 2 * c + e] = m[t][e];
+                ml[(warp * 2 + 1) * C::HEADS + t * 8 + 2 * c + e] = l[t][e];
+            }
+        }
+    __syncthreads();  // every ring is empty: the shares go there
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                int d;
+                if constexpr (!C::I8)
+                    d = i * 16 + g + 8 * (e >> 1);
+                else if constexpr (D == 64)
+                    d = g * 8 + i + 4 * (e >> 1);
+                else
+                    d = (i / 8) * 128 + g * 16 + i % 8 + 8 * (e >> 1);
+                os[(warp * C::HEADS + t * 8 + 2 * c + (e & 1)) * C::OROW + d] = o[t][i][e];
+            }
+}
+
+// The same with the heads on the M side, for groups of 16 or 32 columns of 16-bit caches:
+//   S[16 heads x 8 tokens] = Q[16 x D] . K^T[D x 8]     (A = q, B = K tile)
+//   O[16 heads x D]       += P[16 x 16 tokens] . V[16 x D]  (A = p, B = V tile)
+// P's fragments are S's accumulators as they stand, a row's maximum lies in four lanes instead of
+// eight, and q's fragments take half as many reads, which is what bounded the form above at 32
+// heads (shared-memory reads and exchanges between lanes).
+template <typename T, int D, int NT, int NWARPS, typename Arrived, typename Issue>
+__device__ __forceinline__ void stream_heads_m(const SparseArgs &a, unsigned char *smem, int cnt, Arrived arrived,
+                                               Issue issue) {
+    using C = AttendCfg<T, T, D, NT, NWARPS>;
+    constexpr int S = C::S, NB = C::NB, KS = D / 16, ML = NT / 2, NTK = 2 * NB;  // m-tiles of heads, n-tiles of tokens
+    constexpr bool SPLIT_P = !std::is_same<T, __half>::value;
+    constexpr bool QR = ML * KS <= 8;  // q fragments in registers
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const uint32_t sb = smem_addr(smem);
+    const float kNegInf = __int_as_float(0xff800000);
+    auto qfrag = [&](int t, int ks, uint32_t (&f)[4]) {
+        ldsm_x4(f, sb + C::Q_OFF + (t * 16 + (lane & 15)) * C::QROW + ks * 32 + (lane >> 4) * 16);
+    };
+    uint32_t qa[QR ? ML : 1][QR ? KS : 1][4];
+    if constexpr (QR) {
+#pragma unroll
+        for (int t = 0; t < ML; ++t)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) qfrag(t, ks, qa[t][ks]);
+    }
+    float o[ML][D / 8][4] = {};
+    float m[ML][2], l[ML][2];  // rows g and g + 8
+#pragma unroll
+    for (int t = 0; t < ML; ++t) {
+        m[t][0] = m[t][1] = kNegInf;
+        l[t][0] = l[t][1] = 0.f;
+    }
+    for (int k = 0; k < cnt; k += NB) {
+        int valid[NB];
+        uint32_t kt[NB], vt[NB];
+        bool whole;
+        if (!arrived(k, valid, kt, vt, whole)) break;
+        // ---- S ----
+        float x[ML][NTK][4] = {};
+        const int krow = (lane & 7) + ((lane >> 4) & 1) * 8;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            uint32_t qf[ML][4];
+            if constexpr (!QR) {
+#pragma unroll
+                for (int t = 0; t < ML; ++t) qfrag(t, ks, qf[t]);
+            }
+            const int ch = ks * 2 + ((lane >> 3) & 1);
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+                uint32_t kf[4];
+                ldsm_x4(kf, swz(kt[n1] + (ch >> 3) * 2048, krow, ch & 7));
+#pragma unroll
+                for (int t = 0; t < ML; ++t) {
+                    uint32_t af[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (QR)
+                            af[e] = qa[t][ks][e];
+                        else
+                            af[e] = qf[t][e];
+                    }
+                    Mma<T>::mma(x[t][2 * n1], af, kf[0], kf[1]);
+                    Mma<T>::mma(x[t][2 * n1 + 1], af, kf[2], kf[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < ML; ++t)
+#pragma unroll
+            for (int n = 0; n < NTK; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[t][n][e] *= a.scale_log2;
+        if (!whole) {  // tokens past the last one hold anything, NaN among it
+#pragma unroll
+            for (int n = 0; n < NTK; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if ((n & 1) * 8 + 2 * c + e >= valid[n / 2]) {
+#pragma unroll
+                        for (int t = 0; t < ML; ++t) x[t][n][e] = x[t][n][2 + e] = kNegInf;
+                    }
+        }
+        // ---- running maximum and sum (the reference moves only when it grew by more than 2^8) ----
+        float mx[ML][2];
+        bool grew = false;
+#pragma unroll
+        for (int t = 0; t < ML; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                mx[t][r] = fmaxf(x[t][0][2 * r], x[t][0][2 * r + 1]);
+#pragma unroll
+                for (int n = 1; n < NTK; ++n) mx[t][r] = fmaxf(mx[t][r], fmaxf(x[t][n][2 * r], x[t][n][2 * r + 1]));
+            }
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1)
+#pragma unroll
+            for (int t = 0; t < ML; ++t)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) mx[t][r] = fmaxf(mx[t][r], __shfl_xor_sync(0xffffffffu, mx[t][r], d));
+#pragma unroll
+        for (int t = 0; t < ML; ++t)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) grew |= mx[t][r] > m[t][r] + 8.f;
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int t = 0; t < ML; ++t) {
+                float al[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float mn = mx[t][r] > m[t][r] + 8.f ? mx[t][r] : m[t][r];
+                    al[r] = m[t][r] == mn ? 1.f : fast_exp2(m[t][r] - mn);
+                    m[t][r] = mn;
+                    l[t][r] *= al[r];
+                }
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[t][i][e] *= al[e >> 1];
+            }
+        }
+        uint32_t ph[ML][NB][4], pl[SPLIT_P ? ML : 1][SPLIT_P ? NB : 1][4];
+#pragma unroll
+        for (int t = 0; t < ML; ++t) {
+            float mu[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) mu[r] = m[t][r] == kNegInf ? 0.f : m[t][r];
+#pragma unroll
+            for (int n = 0; n < NTK; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float &p0 = x[t][n][2 * r], &p1 = x[t][n][2 * r + 1];
+                    p0 = fast_exp2(p0 - mu[r]);
+                    p1 = fast_exp2(p1 - mu[r]);
+                    l[t][r] += p0 + p1;
+                    const uint32_t hi = Mma<T>::pack(p0, p1);
+                    ph[t][n / 2][(n & 1) * 2 + r] = hi;
+                    if constexpr (SPLIT_P)
+                        pl[t][n / 2][(n & 1) * 2 + r] =
+                            Mma<T>::pack(p0 - __uint_as_float(hi << 16), p1 - __uint_as_float(hi & 0xffff0000u));
+                }
+        }
+        // ---- O ----
+        if (!whole) zero_rows_past<C, NB>(vt, valid, lane);
+        const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const int ch = i * 2 + (lane >> 4);
+#pragma unroll
+            for (int n1 = 0; n1 < NB; ++n1) {
+                uint32_t vf[4];
+                ldsm_x4_t(vf, swz(vt[n1] + (ch >> 3) * 2048, vrow, ch & 7));
+#pragma unroll
+                for (int t = 0; t < ML; ++t) {
+                    Mma<T>::mma(o[t][2 * i], ph[t][n1], vf[0], vf[1]);
+                    Mma<T>::mma(o[t][2 * i + 1], ph[t][n1], vf[2], vf[3]);
+                    if constexpr (SPLIT_P) {
+                        Mma<T>::mma(o[t][2 * i], pl[t][n1], vf[0], vf[1]);
+                        Mma<T>::mma(o[t][2 * i + 1], pl[t][n1], vf[2], vf[3]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int n1 = 0; n1 < NB; ++n1) issue(k + S + n1);
+    }
+    // ---- this warp's share, for the joining ----
+    float *os = reinterpret_cast<float *>(smem);
+    float *ml = reinterpret_cast<float *>(smem + C::ML_OFF);
+#pragma unroll
+    for (int t = 0; t < ML; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+#pragma unroll
+            for (int d = 1; d < 4; d <<= 1) l[t][r] += __shfl_xor_sync(0xffffffffu, l[t][r], d);
+            if (c == 0) {
+                ml[warp * 2 * C::HEADS + t * 16 + g + 8 * r] = m[t][r];
+                ml[(warp * 2 + 1) * C::HEADS + t * 16 + g + 8 * r] = l[t][r];
+            }
+        }
+    __syncthreads();  // every ring is empty: the shares go there
+#pragma unroll
+    for (int t = 0; t < ML; ++t)
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<float2 *>(os + (warp * C::HEADS + t * 16 + g + 8 * r) * C::OROW + i * 8 + 2 * c) =
+                    make_float2(o[t][i][2 * r], o[t][i][2 * r + 1]);
+}
+
 // The barriers of the warps' rings; before attend_row, and before the previous kernel is waited for.
 template <typename C>
 __device__ __forceinline__ void attend_init(unsigned char *smem) {
@@ -177,9 +674,8 @@ template <typename T, typename TKV, int D, int NT, int NWARPS>
 __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CUtensorMap *tmV, int r, int h, int grp,
                            int rank, int ncta, unsigned char *smem) {
     using C = AttendCfg<T, TKV, D, NT, NWARPS>;
-    constexpr int NW = C::NW, S = C::S, NB = C::NB, KS = D / 16, MT = D / 16;
-    constexpr bool SPLIT_P = !std::is_same<T, __half>::value;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+    constexpr int NW = C::NW, S = C::S, NB = C::NB;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t sb = smem_addr(smem);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF) + warp * S;
     int *info = reinterpret_cast<int *>(smem + C::INFO_OFF) + warp * S;
@@ -279,37 +775,8 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
         }
     }
     __syncthreads();
-    // B fragments of k-steps ks (and, 16-bit caches, ks + 1) of n-tile t, the dims in the order of
-    // the K fragments
-    auto qfrag = [&](int t, int ks, uint32_t (&f)[4]) {
-        if constexpr (!C::I8) {
-            ldsm_x4(f, sb + C::Q_OFF + (t * 8 + (lane & 7)) * C::QROW + ks * 32 + (lane >> 3) * 16);
-        } else {
-            // thread column c reads 32 (D = 64: 16) contiguous bytes per 128-byte segment of a row
-            const int d0 = D == 64 ? c * 16 + ks * 4 : (ks / 8) * 128 + c * 32 + (ks % 8) * 4;
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                         : "r"(sb + C::Q_OFF + (t * 8 + g) * C::QROW + d0 * 2)
-                         : "memory");
-        }
-    };
-    uint32_t qb[C::QREG ? NT : 1][C::QREG ? KS / 2 : 1][4];
-    if constexpr (C::QREG) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int ks = 0; ks < KS; ks += 2) qfrag(t, ks, qb[t][ks / 2]);
-    }
-
-    float o[NT][MT][4] = {};
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        m[t][0] = m[t][1] = __int_as_float(0xff800000);
-        l[t][0] = l[t][1] = 0.f;
-    }
-
-    for (int k = 0; k < cnt; k += NB) {
+    // blocks k .. k + NB - 1: waits for their copies; false: give up
+    auto arrived = [&](int k, int (&valid)[NB], uint32_t (&kt)[NB], uint32_t (&vt)[NB], bool &whole) -> bool {
         bool landed = true;
 #pragma unroll
         for (int n1 = 0; n1 < NB; ++n1)
@@ -318,11 +785,9 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
             // the copies still in flight are waited for, again with a limit, so that none lands
             // in memory that the joining reuses
             for (int i = NB; i < S && k + i < cnt; ++i) mbar_wait(&bars[(k + i) % S], ((k + i) / S) & 1, a.wait_ns);
-            break;
+            return false;
         }
-        int valid[NB];
-        uint32_t kt[NB], vt[NB];
-        bool whole = true;
+        whole = true;
 #pragma unroll
         for (int n1 = 0; n1 < NB; ++n1) {
             const int s = (k + n1) % S;
@@ -331,258 +796,14 @@ __device__ void attend_row(const SparseArgs &a, const CUtensorMap *tmK, const CU
             kt[n1] = ring + s * C::STAGE;
             vt[n1] = kt[n1] + C::TILE;
         }
-        // ---- S^T ----
-        float x[NB][NT][4];
-#pragma unroll
-        for (int n1 = 0; n1 < NB; ++n1)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[n1][t][e] = 0.f;
-#pragma unroll
-        for (int k2 = 0; k2 < KS; k2 += 2) {
-            uint32_t qf[C::QREG ? 1 : NT][4];
-            if constexpr (!C::QREG) {
-#pragma unroll
-                for (int t = 0; t < NT; ++t) qfrag(t, k2, qf[t]);
-            }
-#pragma unroll
-            for (int n1 = 0; n1 < NB; ++n1) {
-                uint32_t af[2][4];
-                if constexpr (!C::I8) {
-                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int ch = (k2 + u) * 2 + (lane >> 4);
-                        ldsm_x4(af[u], swz(kt[n1] + (ch >> 3) * 2048, row, ch & 7));
-                    }
-                } else {
-                    // 8 bytes of tokens g and g + 8
-                    uint32_t wa[2], wb[2];
-                    uint32_t pa, pb;
-                    if constexpr (D == 64) {
-                        pa = kt[n1] + g * 64 + c * 16 + k2 * 4;
-                        pb = pa + 8 * 64;
-                    } else {
-                        const uint32_t seg = kt[n1] + (k2 / 8) * 2048;
-                        pa = swz(seg, g, 2 * c + (k2 % 8) / 4) + (k2 % 4) * 4;
-                        pb = swz(seg, g + 8, 2 * c + (k2 % 8) / 4) + (k2 % 4) * 4;
-                    }
-                    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(wa[0]), "=r"(wa[1]) : "r"(pa) : "memory");
-                    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(wb[0]), "=r"(wb[1]) : "r"(pb) : "memory");
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const uint32_t ua = wa[u] ^ 0x80808080u, ub = wb[u] ^ 0x80808080u;
-                        af[u][0] = i8_pair<T>(ua, 0, 1);
-                        af[u][1] = i8_pair<T>(ub, 0, 1);
-                        af[u][2] = i8_pair<T>(ua, 2, 3);
-                        af[u][3] = i8_pair<T>(ub, 2, 3);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        const uint32_t *f = C::QREG ? qb[t][k2 / 2] : qf[t];
-                        Mma<T>::mma(x[n1][t], af[u], f[2 * u], f[2 * u + 1]);
-                    }
-            }
-        }
-#pragma unroll
-        for (int n1 = 0; n1 < NB; ++n1) {
-            float sc = a.scale_log2;
-            if constexpr (C::I8)
-                sc *= __shfl_sync(0xffffffffu, (k + n1) >> 5 & 1 ? b_ks[1] : b_ks[0], (k + n1) & 31);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[n1][t][e] *= sc;
-        }
-        if (!whole) {  // rows past the last token hold anything, NaN among it
-#pragma unroll
-            for (int n1 = 0; n1 < NB; ++n1)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (g + 8 * (e >> 1) >= valid[n1]) x[n1][t][e] = __int_as_float(0xff800000);
-        }
-        // ---- running maximum and sum; P ----
-        // The reference of the exponentials follows the maximum only when that grew by more than
-        // 2^8: weights of up to 2^8 are as exact, and the output is seldom rescaled.
-        uint32_t ph[NB][NT][2], pl[SPLIT_P ? NB : 1][SPLIT_P ? NT : 1][2];
-        float mx[NT][2];
-        bool grew = false;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float v = fmaxf(x[0][t][e], x[0][t][2 + e]);
-                if constexpr (NB > 1) v = fmaxf(v, fmaxf(x[1][t][e], x[1][t][2 + e]));
-                mx[t][e] = v;
-            }
-#pragma unroll
-        for (int d = 4; d < 32; d <<= 1)
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) mx[t][e] = fmaxf(mx[t][e], __shfl_xor_sync(0xffffffffu, mx[t][e], d));
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) grew |= mx[t][e] > m[t][e] + 8.f;
-        if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                float al[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float mn = mx[t][e] > m[t][e] + 8.f ? mx[t][e] : m[t][e];
-                    al[e] = m[t][e] == mn ? 1.f : fast_exp2(m[t][e] - mn);
-                    m[t][e] = mn;
-                    l[t][e] *= al[e];
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[t][i][e] *= al[e & 1];
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float mu[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) mu[e] = m[t][e] == __int_as_float(0xff800000) ? 0.f : m[t][e];
-#pragma unroll
-            for (int n1 = 0; n1 < NB; ++n1) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[n1][t][e] = fast_exp2(x[n1][t][e] - mu[e & 1]);
-                    l[t][e & 1] += x[n1][t][e];
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {  // tokens g (e = 0) and g + 8, heads 2c, 2c + 1
-                    const uint32_t hi = Mma<T>::pack(x[n1][t][2 * e], x[n1][t][2 * e + 1]);
-                    ph[n1][t][e] = movm_t(hi);
-                    if constexpr (SPLIT_P) {
-                        const float h0 = __uint_as_float(hi << 16), h1 = __uint_as_float(hi & 0xffff0000u);
-                        pl[n1][t][e] = movm_t(Mma<T>::pack(x[n1][t][2 * e] - h0, x[n1][t][2 * e + 1] - h1));
-                    }
-                }
-            }
-        }
-        // ---- O^T ----
-        if constexpr (!C::I8) {
-            if (!whole) {
-                // values behind the last token: a weight of 0 does not make a NaN there 0
-#pragma unroll
-                for (int n1 = 0; n1 < NB; ++n1)
-                    for (int i = lane; i < (kBlockSize - valid[n1]) * (C::ROWB / 16); i += 32) {
-                        const int row = valid[n1] + i / (C::ROWB / 16), ch = i % (C::ROWB / 16);
-                        asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                         swz(vt[n1] + (ch >> 3) * 2048, row, ch & 7)),
-                                     "r"(0)
-                                     : "memory");
-                    }
-                fence_proxy_async_smem();
-                __syncwarp();
-            }
-            const int row = (lane & 7) + ((lane >> 4) & 1) * 8;
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const int ch = i * 2 + ((lane >> 3) & 1);
-#pragma unroll
-                for (int n1 = 0; n1 < NB; ++n1) {
-                    uint32_t af[4];
-                    ldsm_x4_t(af, swz(vt[n1] + (ch >> 3) * 2048, row, ch & 7));
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) {
-                        Mma<T>::mma(o[t][i], af, ph[n1][t][0], ph[n1][t][1]);
-                        if constexpr (SPLIT_P) Mma<T>::mma(o[t][i], af, pl[n1][t][0], pl[n1][t][1]);
-                    }
-                }
-            }
-        } else {
-            constexpr int MS = D == 64 ? 4 : 8, VW = D == 64 ? 2 : 4;  // m-tiles and words per segment
-#pragma unroll
-            for (int n1 = 0; n1 < NB; ++n1) {
-                // a block that is not there: its codes are whatever the stage held, times 0
-                const float vb = __shfl_sync(0xffffffffu, (k + n1) >> 5 & 1 ? b_vs[1] : b_vs[0], (k + n1) & 31);
-                const float vs = valid[n1] > 0 ? vb : 0.f;
-#pragma unroll
-                for (int sg = 0; sg < MT / MS; ++sg) {
-                    uint32_t rw[4][4];  // tokens 2c, 2c + 1, 2c + 8, 2c + 9
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int row = 2 * c + (q & 1) + 8 * (q >> 1);
-                        if constexpr (D == 64) {
-                            asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];"
-                                         : "=r"(rw[q][0]), "=r"(rw[q][1])
-                                         : "r"(vt[n1] + row * 64 + g * 8)
-                                         : "memory");
-                        } else {
-                            lds_v4(rw[q], swz(vt[n1] + sg * 2048, row, g));
-                        }
-#pragma unroll
-                        for (int e = 0; e < VW; ++e) rw[q][e] ^= 0x80808080u;
-                    }
-#pragma unroll
-                    for (int i = 0; i < MS; ++i) {
-                        uint32_t af[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {  // token pair q / 2, dims row (q & 1 ? g + 8 : g)
-                            const int p = q >> 1, wd = (q & 1) * (VW / 2) + i / 4;
-                            const uint32_t sl = (uint32_t)(i & 3) | (uint32_t)(4 + (i & 3)) << 4;
-                            af[q] = i8_pair<T>(__byte_perm(rw[2 * p][wd], rw[2 * p + 1][wd], sl), 0, 1);
-                        }
-#pragma unroll
-                        for (int t = 0; t < NT; ++t) {
-                            float d[4];
-                            Mma<T>::mma0(d, af, ph[n1][t][0], ph[n1][t][1]);
-                            if constexpr (SPLIT_P) Mma<T>::mma(d, af, pl[n1][t][0], pl[n1][t][1]);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[t][sg * MS + i][e] += vs * d[e];
-                        }
-                    }
-                }
-            }
-        }
-        __syncwarp();
-#pragma unroll
-        for (int n1 = 0; n1 < NB; ++n1) issue(k + S + n1);
-    }
-
-    // ---- this warp's share, then the joining ----
-    float *os = reinterpret_cast<float *>(smem);
-    float *ml = reinterpret_cast<float *>(smem + C::ML_OFF);
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l[t][e] += __shfl_xor_sync(0xffffffffu, l[t][e], d);
-            if (g == 0) {
-                ml[warp * 2 * C::HEADS + t * 8 + 2 * c + e] = m[t][e];
-                ml[(warp * 2 + 1) * C::HEADS + t * 8 + 2 * c + e] = l[t][e];
-            }
-        }
-    __syncthreads();  // every ring is empty: the shares go there
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                int d;
-                if constexpr (!C::I8)
-                    d = i * 16 + g + 8 * (e >> 1);
-                else if constexpr (D == 64)
-                    d = g * 8 + i + 4 * (e >> 1);
-                else
-                    d = (i / 8) * 128 + g * 16 + i % 8 + 8 * (e >> 1);
-                os[(warp * C::HEADS + t * 8 + 2 * c + (e & 1)) * C::OROW + d] = o[t][i][e];
-            }
-    join_shares<T, D, C::HEADS, C::OROW, NW>(a, os, ml, ncol, row0, rank, ncta);
+        return true;
+    };
+    if constexpr (NT >= 2 && !C::I8)
+        stream_heads_m<T, D, NT, NWARPS>(a, smem, cnt, arrived, issue);
+    else
+        stream_tokens_m<T, TKV, D, NT, NWARPS>(a, smem, cnt, b_ks, b_vs, arrived, issue);
+    join_shares<T, D, C::HEADS, C::OROW, NW>(a, reinterpret_cast<float *>(smem), reinterpret_cast<float *>(smem + C::ML_OFF),
+                                             ncol, row0, rank, ncta);
 }
 
 // fp32 caches: the same on the CUDA cores, GT query heads at a time, tiles read from global
