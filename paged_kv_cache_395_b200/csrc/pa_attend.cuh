@@ -10,14 +10,16 @@
 // CTA's warps through shared memory, then the cluster's CTAs through distributed shared
 // memory.  So a row needs no workspace and one launch, and the order of every sum is fixed.
 //
-// Tensor-core form (mma.sync m16n8k16, 8 heads per n-tile, NT n-tiles):
-//   S^T[16 tokens x heads] = K[16 x D] . Q^T[D x heads]     (A = K tile, B = q)
-//   O^T[D x heads]        += V^T[D x 16] . P^T[16 x heads]  (A = V tile^T, B = p)
-// so the accumulators of up to 8 heads take D / 4 registers, and every tile is read from
-// shared memory once for all heads.  bf16 rounds P to 8 bits, too few for the result's own
-// precision, so there P = hi + lo, two products; fp16's 11 bits are enough.  An int8 tile's
-// codes become exact fp16 / bf16 fragments in registers; the block's K scale multiplies the
-// scores, its V scale the block's product, in fp32.
+// Tensor-core form (mma.sync m16n8k16, fp32 accumulators, NT * 8 query heads): with the tokens
+// on the M side for up to 8 heads and for int8 caches (stream_tokens_m), with the heads there for
+// 16 or 32 (stream_heads_m); either way a tile is read from shared memory once for all heads.
+// bf16 rounds P to 8 bits, too few for the result's own precision, so there P = hi + lo, two
+// products; fp16's 11 bits are enough.  An int8 tile's codes become exact fp16 / bf16 fragments in
+// registers; the block's K scale multiplies the scores, its V scale the block's product, in fp32.
+//
+// Bound by DRAM where there are rows enough (64 rows x 64 fp16 blocks of 16 x 128: 39.8 us, 5.9
+// TB/s), by the chain list -> table entry -> tiles -> joining where there are few (8 rows: about
+// 5 us), and for int8 by instructions (128 rows x 128 blocks 19.1 us, 3.5 TB/s).
 #pragma once
 #include <cooperative_groups.h>
 

@@ -16,8 +16,9 @@
 // handed out.  Blocks are pushed before they are popped; the cluster's barrier, which also
 // makes the pushes visible, stands between the two.  The slots of a step with few tokens are
 // written by the same launch.  A step with prompts has so many that a cluster's few SMs
-// would be the bound (526k slots: 85 us), so a second kernel writes them over the whole GPU,
-// from the tables and lengths that the first one left.
+// would be the bound, so a second kernel writes them over the whole GPU, from the tables and
+// lengths that the first one left (1024 sequences, 256 of them prompts, 526k slots: 102 us in one
+// cluster of 8 CTAs, 24.5 us this way; 64 sequences of one token: 7.0 us).
 #include <cooperative_groups.h>
 
 #include <atomic>
