@@ -1,5 +1,6 @@
 // pa_decode_selected: decode attention over chosen blocks (pa_attend.cuh).
 #include "pa_attend.cuh"
+#include "pa_cluster.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -44,33 +45,12 @@ __global__ void __launch_bounds__(128) attend_f32_kernel(const SparseArgs a) {
     attend_row_f32<D, GT>(a, (int)(rh / a.H), (int)(rh % a.H), grp, (int)cl.block_rank(), ncta, smem);
 }
 
-// CTAs per row: as many as the GPU holds at once (`slots`), each warp with at least two blocks.  A
-// second, partial wave costs more than the idle slots: 128 rows of 128 int8 blocks on 444 slots took
-// 25.5 us with one CTA a row, 24.4 with two, 20.8 with three and 28.2 with four.
-int cluster_of(int64_t items, int K, int64_t slots, int warps) {
-    int64_t c = slots / items;
-    const int64_t most = K / (2 * warps);
-    if (c > most) c = most;
-    return c < 1 ? 1 : c > 8 ? 8 : (int)c;
-}
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kern)(KArgs...), int64_t ctas, int c, int threads, size_t smem, cudaStream_t st,
-                           Args &&...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = c;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = c > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+// CTAs per row: as many as the GPU holds at once, each warp with at least two blocks.  (128 rows of 128
+// int8 blocks in CTAs of four warps took 25.5 us with one CTA a row, 24.4 with two, 20.8 with three
+// and 28.2 with four, which no longer fit at once.)
+template <typename K>
+int cluster_of(ClusterRoom &room, K *kern, int64_t items, int blocks, int warps, size_t smem) {
+    return room.largest(kern, items, blocks / (2 * warps), warps * 32, smem);
 }
 
 // Map over a cache as tiles of [16 rows][D], one copy per tile: box (128 bytes of a row, 16 rows,
@@ -102,19 +82,22 @@ int launch_attend_t(SparseArgs a, cudaStream_t st) {
     // About a row per SM: one CTA with as many warps as the registers and shared memory hold, instead
     // of a cluster of smaller ones that have to join their shares (128 int8 rows of 128 blocks 19.1 us
     // against 19.8 with three CTAs of four warps; 128 rows of 32 heads 27.8 against 29.2 with their
-    // choice; with fewer rows, in clusters, it is the slower form: 15.5 against 14.8 for 8 rows).
+    // choice).  Fewer rows with long lists: clusters of 8-warp CTAs, so that eight CTAs are 64 warps
+    // (8 rows of 128 blocks 5.6 against 6.3 us, of 256 blocks 7.1 against 8.7, but of 64 blocks 5.3
+    // against 5.1; with 16 or 32 heads a tile it is the slower form: 9.2 against 8.9).
     constexpr int WIDE = NT == 1 ? 12 : 8;
     if constexpr (D <= 128 && NW == 4) {
         const int64_t items = (int64_t)a.rows * a.H * ((a.G + C::HEADS - 1) / C::HEADS);
         if (items <= 148 && 2 * items > 148 && a.K >= 2 * WIDE) return launch_attend_t<T, TKV, D, NT, WIDE>(a, st);
+        if constexpr (NT == 1)
+            if (2 * items <= 148 && a.K >= 128) return launch_attend_t<T, TKV, D, NT, 8>(a, st);
     }
     a.ng = (a.G + C::HEADS - 1) / C::HEADS;
     const int64_t items = (int64_t)a.rows * a.H * a.ng;
     auto kern = attend_kernel<T, TKV, D, NT, NW>;
     if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), C::BYTES)) return PA_ERR_CUDA;
-    int sms, per_sm;
-    if (!tc_launch_shape(reinterpret_cast<const void *>(kern), C::NW * 32, C::BYTES, &sms, &per_sm)) return PA_ERR_CUDA;
-    const int c = cluster_of(items, a.K, (int64_t)sms * per_sm, C::NW);
+    static ClusterRoom room;
+    const int c = cluster_of(room, kern, items, a.K, C::NW, C::BYTES);
     CUtensorMap tk, tv;
     if (!tile_map(&tk, a.kc, a.N * a.H, D, a.kv_dtype) || !tile_map(&tv, a.vc, a.N * a.H, D, a.kv_dtype)) return PA_ERR_CUDA;
     return launch_cluster(kern, items * c, c, C::NW * 32, C::BYTES, st, tk, tv, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -142,9 +125,8 @@ int launch_attend_f32_t(SparseArgs a, cudaStream_t st) {
     const int64_t items = (int64_t)a.rows * a.H * a.ng;
     auto kern = attend_f32_kernel<D, GT>;
     if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), C::BYTES)) return PA_ERR_CUDA;
-    int sms, per_sm;
-    if (!tc_launch_shape(reinterpret_cast<const void *>(kern), C::NW * 32, C::BYTES, &sms, &per_sm)) return PA_ERR_CUDA;
-    const int c = cluster_of(items, a.K, (int64_t)sms * per_sm, C::NW);
+    static ClusterRoom room;
+    const int c = cluster_of(room, kern, items, a.K, C::NW, C::BYTES);
     return launch_cluster(kern, items * c, c, C::NW * 32, C::BYTES, st, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 

@@ -2,6 +2,7 @@
 // decode.
 #include <cooperative_groups.h>
 
+#include "pa_cluster.cuh"
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -242,35 +243,25 @@ __global__ void __launch_bounds__(NT, NT <= 256 && D <= 128 ? 768 / NT : 1) sele
 }
 
 template <typename T, int D, int NT>
-int launch_select_n(const SparseArgs &a, int c, size_t smem, cudaStream_t st) {
+int launch_select_n(const SparseArgs &a, int most, size_t smem, cudaStream_t st) {
     auto kern = select_kernel<T, D, NT>;
     if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), 227 * 1024)) return PA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.rows * a.H * c));
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = c;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = c > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+    const int64_t items = (int64_t)a.rows * a.H;
+    static ClusterRoom room;  // of the shared memory that leaves each SM to one CTA of 512 threads anyway
+    const int c = NT < 512 ? most : room.largest(kern, items, most, NT, 100 * 1024);
+    return launch_cluster(kern, items * c, c, NT, smem, st, a) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 template <typename T, int D>
 int launch_select_t(const SparseArgs &a, cudaStream_t st) {
     const int nblk = (a.max_len + kBlockSize - 1) / kBlockSize;
     const int64_t items = (int64_t)a.rows * a.H;
+    static_assert(SelectSmem<D>::bytes(64, PA_SPARSE_MAX_SEQ_LEN / kBlockSize) <= 227 * 1024, "keys of the longest row");
+    const size_t smem = SelectSmem<D>::bytes(a.G, nblk);
     // CTAs per row: as many as give every SM one, each with at least 128 boxes to score
     int c = (int)(items < 148 ? 148 / items : 1);
     if (c > 8) c = 8;
     while (c > 1 && nblk / c < 128) --c;
-    const size_t smem = SelectSmem<D>::bytes(a.G, nblk);
-    static_assert(SelectSmem<D>::bytes(64, PA_SPARSE_MAX_SEQ_LEN / kBlockSize) <= 227 * 1024, "keys of the longest row");
     // Threads: 512 where the SMs have a CTA each at most, with more than a tile for each of 8 warps
     // (128 rows of 256 blocks 5.8 us, with two CTAs of 256 threads a row 7.0; of 512 blocks 7.1 against
     // 9.1), or where a CTA's boxes are many; 128 for very many short rows, whose picking is then

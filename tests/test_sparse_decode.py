@@ -160,10 +160,12 @@ def test_attention_over_chosen_blocks(dtype, cache, d, H, G):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,cache", [("float16", None), ("bfloat16", None), ("float32", None), ("float16", "int8")])
-@pytest.mark.parametrize("B,L,K", [(1, 5000, 300), (1, 5000, 17), (3, 3000, 64), (40, 700, 30)])
-def test_rows_split_over_ctas(dtype, cache, B, L, K):
-    """From one CTA per row to eight; more blocks per warp than one batch of 32."""
-    w = Case([L + 3 * b for b in range(B)], 2, 4, 128, dtype, cache, seed=L + B)
+@pytest.mark.parametrize("B,L,K,d", [(1, 5000, 300, 128), (1, 5000, 17, 128), (3, 3000, 64, 128), (40, 700, 30, 128),
+                                     (1, 40000, 2500, 64), (8, 3000, 150, 64), (11, 2300, 128, 128), (35, 2100, 130, 64)])
+def test_rows_split_over_ctas(dtype, cache, B, L, K, d):
+    """From one CTA per row to eight, of four and eight warps; more blocks per warp than one batch
+    of 32."""
+    w = Case([L + 3 * b for b in range(B)], 2, 4, d, dtype, cache, seed=L + B)
     sel, cnt = w.lists(K, 5)
     w.check(w.attend(sel, cnt), w.model(sel, cnt), w.attend(sel, cnt, True))
 
