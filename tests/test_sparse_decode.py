@@ -534,3 +534,27 @@ def test_two_graphs_and_an_eager_call():
         eager = a.sparse(11, 1, 2)[0]
     torch.cuda.synchronize()
     assert np.array_equal(bits(outs[0]), bits(eager)) and np.array_equal(bits(outs[1]), bits(b.sparse(40, 1, 2)[0]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache", [("float16", None), ("float32", None), ("bfloat16", "int8")])
+def test_nothing_to_see(dtype, cache):
+    """max_seq_len 0, or lengths of 0 and below: zeros and empty lists."""
+    w = Case([40, 300], 2, 2, 64, dtype, cache, seed=2)
+    for lens, max_len in (([40, 300], 0), ([0, -3], 300), ([-2147483648, 0], 300)):
+        w.max_len = max_len
+        w.dev["lens"] = to_dev(np.array(lens, np.int32), "i")
+        out, sel, cnt = w.sparse(9, 1, 2)
+        assert (out == 0).all() and (sel == -1).all() and (cnt == 0).all()
+        assert (w.attend(*w.lists(9)) == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("d,G", [(128, 4), (64, 20), (256, 3)])
+def test_several_new_tokens_on_an_int8_cache(dtype, d, G):
+    w = Case([2, 17, 33, 500], 2, G, d, dtype, "int8", Q=2, seed=G)
+    out, s, c = w.sparse(8, 1, 2)
+    want = M.choose(w.qf, w.codes, w.bs, w.tables, w.lens, 8, 1, 2, w.max_len)
+    assert np.array_equal(s, want[0]) and np.array_equal(c, want[1])
+    w.check(out, w.model(s, c), w.sparse(8, 1, 2, True)[0])
