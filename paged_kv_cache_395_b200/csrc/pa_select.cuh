@@ -319,7 +319,9 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
                 cut = kl;
                 break;
             }
-            kh = min(kh, kl + ((1u << sh) - 1));
+            // the bin's end, from the distance: kl + 2^sh - 1 itself may pass 2^32 (bins of 2^24 keys
+            // below +inf, the key of every block whose box is not finite)
+            kh = kl + min(kh - kl, (1u << sh) - 1);
             if (in <= S::CAND) {
                 // the bin's keys, ranked against each other
                 for (int j = f0 + tid; j < f1; j += NT) {
@@ -350,7 +352,7 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
     }
 
     // ---- the picks in index order: every thread a run of the row (of odd length: the lanes' reads
-    // fall into different banks) ----
+    // fall into different banks); K of them in all, and none is written past the row's list ----
     const int run = (n + NT - 1) / NT | 1, r0 = min(n, tid * run), r1 = min(n, r0 + run);
     auto cls = [&](int j) {  // 2: taken, 1: equal to the cut
         const uint32_t k = keys[j];
@@ -391,12 +393,12 @@ __device__ void select_row(const SparseArgs &a, int r, int h, int rank, int ncta
     if (run <= 32) {
         for (uint32_t all = gm | em; all; all &= all - 1) {
             const uint32_t bit = all & -all;
-            if ((gm & bit) || eqs++ < (uint32_t)need) out[at++] = r0 + __ffs(bit) - 1;
+            if (((gm & bit) || eqs++ < (uint32_t)need) && at < (uint32_t)K) out[at++] = r0 + __ffs(bit) - 1;
         }
     } else if (gt + eq) {
         for (int j = r0; j < r1; ++j) {
             const int k = cls(j);
-            if (k == 2 || (k == 1 && eqs++ < (uint32_t)need)) out[at++] = j;
+            if ((k == 2 || (k == 1 && eqs++ < (uint32_t)need)) && at < (uint32_t)K) out[at++] = j;
         }
     }
     if (tid == 0) a.nsel[(size_t)r * a.H + h] = K;

@@ -323,3 +323,62 @@ def test_lengths_past_the_bounds_are_cut():
         got = run_select(q, "float16", codes, scales, tables, given, 7, 1, 1, max_len)
         want = M.choose(M.values(q), codes, scales, tables, given, 7, 1, 1, max_len)
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("low", ["minus one", "minus infinity", "a bad block", "nothing"])
+@pytest.mark.parametrize("n,infs,K", [(60, 20, 13), (700, 600, 13), (700, 512, 13), (700, 513, 515), (9000, 5000, 3000),
+                                      (9000, 300, 40)])
+def test_more_boxes_that_are_not_finite_than_picks(n, infs, K, low):
+    """Every box that is not finite scores +inf, the largest key there is, whose histogram bin ends
+    at the top of the keys' 32 bits: with more of them than picks the cut lies in that bin, whatever
+    the lowest score of the row makes the bins' width.  The row behind keeps its list."""
+    d, N = 64, 64
+    rng = np.random.default_rng(n + infs)
+    codes, scales = M.boxes(rng.standard_normal((N, 1, BS, d)).astype(np.float32) + np.float32(2))
+    scales[:8] = np.inf
+    codes[:8] = 0
+    tables = rng.integers(8 if low == "nothing" else 9, N, (1, n)).astype(np.int32)
+    tables[0, rng.permutation(np.arange(1, n - 2))[:infs]] = rng.integers(0, 8, infs)
+    if low in ("minus one", "minus infinity"):
+        codes[8], scales[8] = -127, np.float32(1e-3 if low == "minus one" else 1e38)
+        tables[0, 5] = 8
+    elif low == "a bad block":
+        tables[0, 5] = -1
+    q = np.ones((1, 1, 2, d), np.float16)
+    sel = torch.full((2, 1, K), 99, dtype=torch.int32, device="cuda")
+    cnt = torch.full((2, 1), 99, dtype=torch.int32, device="cuda")
+    pa.pa_get_error_flags(reset=True)
+    pa.pa_select_blocks(sel[:1], cnt[:1], to_dev(q, "float16")[0], to_dev(codes, "i"), to_dev(scales, "f"), to_dev(tables, "i"),
+                        torch.tensor([n * BS], dtype=torch.int32, device="cuda"), n * BS, 1, 2)
+    assert pa.pa_get_error_flags(reset=True) == (pa.PA_EFLAG_BAD_BLOCK if low == "a bad block" else 0)
+    want = M.choose(M.values(q), codes, scales, tables, [n * BS], K, 1, 2, n * BS)
+    assert np.array_equal(sel[:1].cpu().numpy(), want[0][0]) and int(cnt[0]) == K
+    assert (sel[1] == 99).all() and int(cnt[1]) == 99
+
+
+def narrowed(keys, need, kl, kh):
+    """The picker's narrowing of the cut, in Python's whole numbers with the kernel's 32-bit
+    wrap-around: the range it ends with and the keys inside that it expects there."""
+    while True:
+        sh = max(0, (kh - kl).bit_length() - 8)
+        hist = np.bincount((keys[(keys >= kl) & (keys <= kh)] - kl) >> sh, minlength=256)
+        assert len(hist) == 256
+        above = np.concatenate((np.cumsum(hist[::-1])[::-1][1:], [0]))
+        (b,) = np.flatnonzero((above < need) & (above + hist >= need))
+        need -= int(above[b])
+        kl += int(b) << sh
+        kh = (kl + min(kh - kl, (1 << sh) - 1)) & 0xffffffff
+        if hist[b] == need or sh == 0 or hist[b] <= 512:
+            return kl, kh, int(hist[b])
+
+
+@pytest.mark.parametrize("low", [0, 0x007fffff, 0x407fffff, 0x7fffffff, 0xff7fffff, 0xff800000])
+@pytest.mark.parametrize("infs", [20, 513, 5000])
+def test_the_cut_stays_in_range(low, infs):
+    """The bin that holds the cut, its end among 32-bit keys, holds the keys that were counted."""
+    keys = np.full(infs + 1, 0xff800000, np.int64)
+    keys[3] = low
+    for need in (1, 10, infs - 1):
+        kl, kh, n = narrowed(keys, need, int(keys.min()), int(keys.max()))
+        assert kl <= kh and ((keys >= kl) & (keys <= kh)).sum() == n
