@@ -450,10 +450,8 @@ int launch_step_tables(const StepArgs &a, cudaStream_t st) {
     const int threads = a.B <= 256 && few ? 256 : 1024;
     const size_t smem = Smem::bytes(a.B);
     auto kern = few ? step_tables_kernel<true> : step_tables_kernel<false>;
-    if (smem > 48 * 1024) {
-        static std::atomic<unsigned long long> done[2];
-        if (!raise_smem(kern, Smem::bytes(PA_STEP_MAX_SEQS), done[few])) return PA_ERR_CUDA;
-    }
+    // Always: the 48 KB that a launch has without it count the kernel's static shared memory too.
+    if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), (int)Smem::bytes(PA_STEP_MAX_SEQS))) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ncta);
     cfg.blockDim = dim3(threads);
