@@ -422,15 +422,6 @@ bool set_once(std::atomic<unsigned long long> &done, F f) {
     return true;
 }
 
-// Raise a kernel's shared-memory limit to `bytes`.
-template <typename K>
-bool raise_smem(K *kern, size_t bytes, std::atomic<unsigned long long> &done) {
-    return set_once(done, [&] {
-        return cudaFuncSetAttribute(reinterpret_cast<const void *>(kern), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)bytes) == cudaSuccess;
-    });
-}
-
 }  // namespace
 
 int launch_step_tables(const StepArgs &a, cudaStream_t st) {
@@ -451,7 +442,10 @@ int launch_step_tables(const StepArgs &a, cudaStream_t st) {
     const size_t smem = Smem::bytes(a.B);
     auto kern = few ? step_tables_kernel<true> : step_tables_kernel<false>;
     // Always: the 48 KB that a launch has without it count the kernel's static shared memory too.
+    // Both kernels' before the first launch, which moves the sequences on: a call that cannot
+    // write its slots must not have done that.
     if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), (int)Smem::bytes(PA_STEP_MAX_SEQS))) return PA_ERR_CUDA;
+    if (!few && !set_smem_attr_once(reinterpret_cast<const void *>(step_slots_kernel), PA_STEP_MAX_SEQS * 8)) return PA_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ncta);
     cfg.blockDim = dim3(threads);
@@ -467,13 +461,8 @@ int launch_step_tables(const StepArgs &a, cudaStream_t st) {
     cfg.numAttrs = ncta > 1 ? 2 : 1;
     if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return PA_ERR_CUDA;
     if (few) return PA_OK;
-    const size_t smem2 = (size_t)a.B * 8;
-    if (smem2 > 48 * 1024) {
-        static std::atomic<unsigned long long> done2;
-        if (!raise_smem(step_slots_kernel, (size_t)PA_STEP_MAX_SEQS * 8, done2)) return PA_ERR_CUDA;
-    }
     const int64_t ctas = ((int64_t)a.T + 2047) / 2048;
-    return launch_pdl(step_slots_kernel, dim3((unsigned)(ctas < 2 * 148 ? ctas : 2 * 148)), dim3(512), smem2, st, a) ==
+    return launch_pdl(step_slots_kernel, dim3((unsigned)(ctas < 2 * 148 ? ctas : 2 * 148)), dim3(512), (size_t)a.B * 8, st, a) ==
                    cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;

@@ -45,3 +45,10 @@ def served(sizes):
 def test_batches_around_the_default_shared_memory(T):
     """The prefix sums take 25 bytes a sequence beside the kernel's own 400."""
     served([(b, T) for b in (1930, 1947, 1948, 1949, 1950, 1964, 1965)])
+
+
+@pytest.mark.gpu
+def test_slots_of_batches_around_the_default_shared_memory():
+    """The launch that writes the slots of a step with many tokens takes 8 bytes a sequence beside
+    its own 256."""
+    served([(b, 9000) for b in (6111, 6112, 6113, 6144, 6145)])
