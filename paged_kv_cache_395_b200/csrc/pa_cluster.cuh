@@ -1,4 +1,4 @@
-// Host helpers of the block-sparse launches: clusters.
+// Host helpers of the launches of thread-block clusters (step tables, block-sparse decode).
 #pragma once
 #include <atomic>
 
@@ -26,12 +26,13 @@ static cudaError_t launch_cluster(void (*kern)(KArgs...), int64_t ctas, int c, i
     return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
-// How many clusters of 1 .. 8 CTAs of one kernel a device holds at once, asked of CUDA once per
-// device and size.  A cluster lies within one GPC, so this is less than the CTAs that fit, and it
+// How many clusters of 1 .. 16 CTAs of one kernel a device holds at once, asked of CUDA once per
+// device and size (above 8, which not every device has room for, the kernel is first allowed them).  A cluster lies within one GPC, so this is less than the CTAs that fit, and it
 // differs from chip to chip: 16 clusters of 8 CTAs, one per SM, are not always there at once.
 struct ClusterRoom {
     static constexpr int kDevices = 64;
-    std::atomic<int> n[kDevices][9] = {};  // 0: not asked yet
+    static constexpr int kMost = 16;
+    std::atomic<int> n[kDevices][kMost + 1] = {};  // 0: not asked yet
 
     // 0 where CUDA does not say.
     template <typename K>
@@ -50,7 +51,9 @@ struct ClusterRoom {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int got = 0;
-        if (cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess) {
+        if ((c > 8 && cudaFuncSetAttribute(reinterpret_cast<const void *>(kern),
+                                           cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+            cudaOccupancyMaxActiveClusters(&got, kern, &cfg) != cudaSuccess) {
             cudaGetLastError();
             return 0;
         }

@@ -21,8 +21,7 @@
 // cluster of 8 CTAs, 24.5 us this way; 64 sequences of one token: 7.0 us).
 #include <cooperative_groups.h>
 
-#include <atomic>
-
+#include "pa_cluster.cuh"
 #include "pa_common.cuh"
 #include "pa_internal.h"
 
@@ -410,34 +409,12 @@ __global__ void __launch_bounds__(512) step_slots_kernel(const StepArgs a) {
     }
 }
 
-// Calls f once per device (again where it failed).
-template <typename F>
-bool set_once(std::atomic<unsigned long long> &done, F f) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (dev < 64 && (done.load() & bit)) return true;
-    if (!f()) return false;
-    done.fetch_or(bit);
-    return true;
-}
-
 }  // namespace
 
 int launch_step_tables(const StepArgs &a, cudaStream_t st) {
     // A step with few tokens is one launch of one CTA: a cluster's barriers and a second launch
     // would only add latency.
     const bool few = a.T <= 4096;
-    // (16 CTAs, beyond the portable 8: the steps with prompts hand out thousands of blocks.)
-    const int ncta = few ? 1 : 16;
-    if (!few) {
-        static std::atomic<unsigned long long> wide;
-        if (!set_once(wide, [] {
-                return cudaFuncSetAttribute(reinterpret_cast<const void *>(step_tables_kernel<false>),
-                                            cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-            }))
-            return PA_ERR_CUDA;
-    }
     const int threads = a.B <= 256 && few ? 256 : 1024;
     const size_t smem = Smem::bytes(a.B);
     auto kern = few ? step_tables_kernel<true> : step_tables_kernel<false>;
@@ -446,20 +423,13 @@ int launch_step_tables(const StepArgs &a, cudaStream_t st) {
     // write its slots must not have done that.
     if (!set_smem_attr_once(reinterpret_cast<const void *>(kern), (int)Smem::bytes(PA_STEP_MAX_SEQS))) return PA_ERR_CUDA;
     if (!few && !set_smem_attr_once(reinterpret_cast<const void *>(step_slots_kernel), PA_STEP_MAX_SEQS * 8)) return PA_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ncta);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ncta;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = ncta > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return PA_ERR_CUDA;
+    // 16 CTAs, beyond the portable 8 (the steps with prompts hand out thousands of blocks), where a
+    // cluster of the largest step's shared memory finds room; half as many, and so on, where not, as
+    // on a slice of a GPU.
+    int ncta = few ? 1 : 16;
+    static ClusterRoom room;
+    while (ncta > 1 && room.of(kern, ncta, 1024, Smem::bytes(PA_STEP_MAX_SEQS)) < 1) ncta /= 2;
+    if (launch_cluster(kern, ncta, ncta, threads, smem, st, a) != cudaSuccess) return PA_ERR_CUDA;
     if (few) return PA_OK;
     const int64_t ctas = ((int64_t)a.T + 2047) / 2048;
     return launch_pdl(step_slots_kernel, dim3((unsigned)(ctas < 2 * 148 ? ctas : 2 * 148)), dim3(512), (size_t)a.B * 8, st, a) ==
