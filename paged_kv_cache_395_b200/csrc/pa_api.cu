@@ -594,13 +594,16 @@ static int sparse_args(const pa_sparse_params *p, SparseArgs *a) {
     if (p->block_size != PA_BLOCK_SIZE || (p->head_dim != 64 && p->head_dim != 128 && p->head_dim != 256) ||
         p->num_q_heads / p->num_kv_heads > 64 || p->max_blocks_per_seq > (1 << 26) ||
         p->max_selected > PA_SPARSE_MAX_SEQ_LEN / PA_BLOCK_SIZE || p->num_kv_heads > 65535 ||
-        (int64_t)p->num_seqs * Q * p->num_kv_heads > (1 << 26) || (p->flags & ~PA_DECODE_OUT_F32))
+        (p->flags & ~PA_DECODE_OUT_F32))
         return PA_ERR_UNSUPPORTED;
+    // rows first: three factors of up to 31 bits pass 64
+    const int64_t rows = (int64_t)p->num_seqs * Q;
+    if (rows > (1 << 26) || rows * p->num_kv_heads > (1 << 26)) return PA_ERR_UNSUPPORTED;
     const int cap = p->max_blocks_per_seq * PA_BLOCK_SIZE;
     *a = SparseArgs{};
     a->max_len = p->max_seq_len < cap ? p->max_seq_len : cap;
     if (a->max_len > PA_SPARSE_MAX_SEQ_LEN) return PA_ERR_UNSUPPORTED;
-    a->rows = p->num_seqs * Q;
+    a->rows = (int)rows;
     a->Q = Q;
     a->Hq = p->num_q_heads;
     a->H = p->num_kv_heads;

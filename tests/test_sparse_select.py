@@ -382,3 +382,16 @@ def test_the_cut_stays_in_range(low, infs):
     for need in (1, 10, infs - 1):
         kl, kh, n = narrowed(keys, need, int(keys.min()), int(keys.max()))
         assert kl <= kh and ((keys >= kl) & (keys <= kh)).sum() == n
+
+
+@pytest.mark.parametrize("kw", [dict(num_seqs=1 << 30, query_len=1 << 30, num_kv_heads=16, num_q_heads=16),
+                                dict(num_seqs=(1 << 31) - 1, query_len=(1 << 31) - 1, num_kv_heads=65535, num_q_heads=65535),
+                                dict(num_seqs=1 << 27, num_kv_heads=1), dict(num_seqs=1, query_len=1 << 27, num_kv_heads=1),
+                                dict(num_seqs=1 << 16, query_len=1 << 16, num_kv_heads=1)])
+def test_row_counts_past_the_limit_are_refused(kw):
+    """Also where the number of (row, KV head) pairs passes 64 bits, or the rows 32."""
+    f = ctypes.c_void_p(FAKE)
+    p = sparse_params(**kw)
+    assert pa.lib.pa_select_blocks(*[f] * 7, ctypes.byref(p), None) == pa.PA_ERR_UNSUPPORTED
+    assert pa.lib.pa_decode_selected(*[f] * 8, 0.1, ctypes.byref(p), None) == pa.PA_ERR_UNSUPPORTED
+    assert pa.lib.pa_decode_sparse(*[f] * 10, 0.1, ctypes.byref(p), None) == pa.PA_ERR_UNSUPPORTED
