@@ -564,10 +564,24 @@ int pa_select_blocks(int32_t *selected, int32_t *num_selected, const void *q, co
  * no token left gives zeros.  Precision, int8 caches and PA_DECODE_OUT_F32 as in pa_decode;
  * num_blocks * num_kv_heads < 2^31.  One launch, no workspace.
  * sink_blocks and recent_blocks of p are checked and not used.
+ * A row of which a copy did not land within one second (PA_EFLAG_WAIT_TIMEOUT) is NaN.
  */
 int pa_decode_selected(void *out, const void *q, const void *key_cache, const void *value_cache,
                        const int32_t *block_tables, const int32_t *seq_lens, const int32_t *selected,
                        const int32_t *num_selected, float scale, const pa_sparse_params *p, pa_stream_t stream);
+
+/*
+ * Self-test of that: pa_decode_selected (fp16 and bf16 q) with every wait for a copy limited to
+ * limit_ns nanoseconds, and the copies of the stall_at-th block of the first warp, in row 0 and KV
+ * head 0, never issued.  Nothing is read or written for that block, and nothing hangs.  Expected
+ * outcome: PA_OK, PA_EFLAG_WAIT_TIMEOUT in the error word, NaN in the first query heads of row 0
+ * (all that run with the first: up to 32 of KV head 0), the other rows as pa_decode_selected gives
+ * them.  stall_at counts the blocks of that warp: where it has fewer, the call is pa_decode_selected.
+ */
+int pa_decode_selected_stall_selftest(void *out, const void *q, const void *key_cache, const void *value_cache,
+                                      const int32_t *block_tables, const int32_t *seq_lens, const int32_t *selected,
+                                      const int32_t *num_selected, float scale, const pa_sparse_params *p, int stall_at,
+                                      uint64_t limit_ns, pa_stream_t stream);
 
 /*
  * pa_select_blocks, then pa_decode_selected with its lists, in one call.  selected and

@@ -666,6 +666,7 @@ static int attend_args(const pa_sparse_params *p, SparseArgs *a, void *out, cons
     a->nsel = nsel;
     a->scale_log2 = scale * kLog2e;
     a->out_f32 = (p->flags & PA_DECODE_OUT_F32) || p->q_dtype == PA_F32 ? 1 : 0;
+    a->stall_at = -1;
     a->wait_ns = kWaitLimitNs;
     return PA_OK;
 }
@@ -684,6 +685,24 @@ int pa_decode_selected(void *out, const void *q, const void *key_cache, const vo
     rc = attend_args(p, &a, out, q, key_cache, value_cache, block_tables, seq_lens, const_cast<int32_t *>(selected),
                      const_cast<int32_t *>(num_selected), scale);
     if (rc != PA_OK) return rc;
+    return launch_decode_selected(a, (cudaStream_t)stream);
+}
+
+int pa_decode_selected_stall_selftest(void *out, const void *q, const void *key_cache, const void *value_cache,
+                                      const int32_t *block_tables, const int32_t *seq_lens, const int32_t *selected,
+                                      const int32_t *num_selected, float scale, const pa_sparse_params *p, int stall_at,
+                                      uint64_t limit_ns, pa_stream_t stream) {
+    SparseArgs a;
+    int rc = sparse_args(p, &a);
+    if (rc != PA_OK) return rc;
+    if (stall_at < 0 || limit_ns == 0) return PA_ERR_SHAPE;
+    if (p->q_dtype == PA_F32) return PA_ERR_UNSUPPORTED;  // plain loads, no waits
+    if (a.rows == 0) return PA_OK;
+    rc = attend_args(p, &a, out, q, key_cache, value_cache, block_tables, seq_lens, const_cast<int32_t *>(selected),
+                     const_cast<int32_t *>(num_selected), scale);
+    if (rc != PA_OK) return rc;
+    a.stall_at = stall_at;
+    a.wait_ns = limit_ns;
     return launch_decode_selected(a, (cudaStream_t)stream);
 }
 

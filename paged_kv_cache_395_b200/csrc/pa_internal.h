@@ -136,6 +136,8 @@ struct SparseArgs {
     float scale_log2;  // scale * log2(e): scores are kept in the log2 domain
     int out_f32;       // out is fp32: PA_DECODE_OUT_F32, or q is
     int ng;            // groups of query heads per KV head that run apart
+    int stall_at;      // -1; else the first warp leaves its stall_at-th block's copies unissued
+                       // (pa_decode_selected_stall_selftest)
     unsigned long long wait_ns;  // limit of every bounded wait on a copy
 };
 int launch_select_blocks(const SparseArgs &a, cudaStream_t st);

@@ -7,7 +7,7 @@ The names mirror the C ABI in ``include/pa.h``:
   ``pa_decode_stall_selftest``, ``pa_block_copy``, ``pa_quantize_int8``,
   ``pa_quantize_int4``, ``pa_append_int8``, ``pa_step_tables``,
   ``pa_block_bounds``, ``pa_select_blocks``, ``pa_decode_selected``, ``pa_decode_sparse``,
-  ``pa_decode_workspace_size``,
+  ``pa_decode_selected_stall_selftest``, ``pa_decode_workspace_size``,
   ``pa_decode_algo``, ``pa_get_error_flags`` take torch CUDA tensors (or raw device pointers via ``lib``), check device,
   dtype and contiguity, and call the library on
   ``torch.cuda.current_stream()``.  Every step of the computation runs in the
@@ -119,6 +119,7 @@ def _load():
     # pa_sparse_params as packed bytes, or a pointer to PaSparseParams
     L.pa_select_blocks.argtypes = [P] * 9
     L.pa_decode_selected.argtypes = [P] * 8 + [f32, P, P]
+    L.pa_decode_selected_stall_selftest.argtypes = [P] * 8 + [f32, P, i32, ctypes.c_uint64, P]
     L.pa_decode_sparse.argtypes = [P] * 10 + [f32, P, P]
     L.pa_get_error_flags.argtypes = [ctypes.POINTER(ctypes.c_uint), i32, P]
     L.pa_status_string.argtypes = [i32]
@@ -128,7 +129,8 @@ def _load():
               "pa_decode_append_fused", "pa_decode_fixed_scratch",
               "pa_decode_stall_selftest", "pa_decode_algo", "pa_decode_launches", "pa_block_copy",
               "pa_quantize_int8", "pa_quantize_int4", "pa_step_tables", "pa_block_bounds", "pa_select_blocks",
-              "pa_decode_selected", "pa_decode_sparse", "pa_get_error_flags", "pa_version"):
+              "pa_decode_selected", "pa_decode_selected_stall_selftest", "pa_decode_sparse", "pa_get_error_flags",
+              "pa_version"):
         getattr(L, n).restype = i32
     return L
 
@@ -140,7 +142,8 @@ EXPORTED = ("pa_reshape_and_cache", "pa_reshape_and_cache_ex", "pa_append_int8",
             "pa_decode_algo", "pa_decode_launches", "pa_decode", "pa_decode_append", "pa_decode_append_fused",
             "pa_decode_fixed_scratch", "pa_decode_stall_selftest", "pa_block_copy", "pa_quantize_int8",
             "pa_quantize_int4", "pa_step_tables", "pa_block_bounds", "pa_select_blocks", "pa_decode_selected",
-            "pa_decode_sparse", "pa_get_error_flags", "pa_status_string", "pa_version")
+            "pa_decode_selected_stall_selftest", "pa_decode_sparse", "pa_get_error_flags", "pa_status_string",
+            "pa_version")
 FIXED_SCRATCH_BYTES = 32 << 20  # PA_FIXED_SCRATCH_BYTES
 
 
@@ -651,6 +654,19 @@ def pa_decode_selected(out, q, key_cache, value_cache, block_tables, seq_lens, s
                                 _raw_stream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "pa_decode_selected")
+
+
+def pa_decode_selected_stall_selftest(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected,
+                                      scale, max_seq_len, stall_at, limit_ns, k_scales=None, v_scales=None, stream=None):
+    """pa_decode_selected with the failure path exercised: the first warp of row 0 leaves the
+    copies of its stall_at-th block unissued, so its bounded wait runs out after limit_ns (see
+    include/pa.h).  Returns after the launch; the error word then holds PA_EFLAG_WAIT_TIMEOUT."""
+    p, _, _, dev = _sparse_decode_params(out, q, key_cache, value_cache, block_tables, seq_lens, selected, num_selected,
+                                         max_seq_len, 0, 1, k_scales, v_scales)
+    _check(lib.pa_decode_selected_stall_selftest(
+        out.data_ptr(), q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(), block_tables.data_ptr(),
+        seq_lens.data_ptr(), selected.data_ptr(), num_selected.data_ptr(), scale, p, int(stall_at), int(limit_ns),
+        _raw_stream(dev) if stream is None else stream.cuda_stream), "pa_decode_selected_stall_selftest")
 
 
 def pa_decode_sparse(out, q, key_cache, value_cache, bounds, bound_scales, block_tables, seq_lens, selected,

@@ -558,3 +558,60 @@ def test_several_new_tokens_on_an_int8_cache(dtype, d, G):
     want = M.choose(w.qf, w.codes, w.bs, w.tables, w.lens, 8, 1, 2, w.max_len)
     assert np.array_equal(s, want[0]) and np.array_equal(c, want[1])
     w.check(out, w.model(s, c), w.sparse(8, 1, 2, True)[0])
+
+
+def test_stall_selftest_refusals():
+    f = ctypes.c_void_p(FAKE)
+
+    def call(p, stall_at=0, limit_ns=1000, args=(f,) * 8):
+        return pa.lib.pa_decode_selected_stall_selftest(*args, 0.1, ctypes.byref(p), stall_at, limit_ns, None)
+
+    assert call(sparse_params(), stall_at=-1) == pa.PA_ERR_SHAPE
+    assert call(sparse_params(), limit_ns=0) == pa.PA_ERR_SHAPE
+    assert call(sparse_params(q_dtype=pa.PA_F32, kv_dtype=pa.PA_F32)) == pa.PA_ERR_UNSUPPORTED
+    assert call(sparse_params(num_seqs=0)) == pa.PA_OK
+    for kw, status in BAD_SPARSE:
+        assert call(sparse_params(**kw)) == status
+    for i in range(8):
+        assert call(sparse_params(), args=tuple(ctypes.c_void_p(None if k == i else FAKE) for k in range(8))) == pa.PA_ERR_NULL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,cache,B,G,d,K", [
+    ("float16", None, 3, 4, 128, 200),    # a cluster a row, eight warps a CTA
+    ("bfloat16", None, 80, 4, 64, 100),   # 12 warps, one CTA a row
+    ("float16", None, 230, 3, 64, 40),    # three warps
+    ("bfloat16", None, 2, 20, 128, 90),   # heads on the M side
+    ("float16", None, 2, 4, 256, 60),     # one block a step
+    ("float16", "int8", 2, 4, 128, 100)])
+@pytest.mark.parametrize("stall_at", [0, 1, 2])
+def test_wait_timeout_of_a_chosen_block(dtype, cache, B, G, d, K, stall_at):
+    """The failure path of the bounded waits, without a fault: one block's copies are left
+    unissued.  Every wait ends, the flag is set, the row is NaN (not a result without that block),
+    the other rows and the next call are as ever."""
+    H = 2
+    w = Case([K * BS + 7 * b % 50 for b in range(B)], H, G, d, dtype, cache, seed=B)
+    sel, cnt = w.lists(K, 1)
+    ref = w.attend(sel, cnt)
+    x = w.dev
+    s = torch.from_numpy(sel).cuda().reshape(w.lead + (H, K)).contiguous()
+    c = torch.from_numpy(cnt).cuda().reshape(w.lead + (H,)).contiguous()
+    out = torch.zeros_like(x["q"])
+    pa.pa_get_error_flags(reset=True)
+    limit_ns = 2_000_000
+    t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    t0.record()
+    pa.pa_decode_selected_stall_selftest(out, x["q"], x["kc"], x["vc"], x["tables"], x["lens"], s, c, w.scale, w.max_len,
+                                         stall_at, limit_ns, k_scales=x["ks"], v_scales=x["vs"])
+    t1.record()
+    torch.cuda.synchronize()
+    # the block's wait, and once more the wait for what is in flight
+    assert t0.elapsed_time(t1) >= 2 * limit_ns / 1e6
+    assert pa.pa_get_error_flags(reset=True) == pa.PA_EFLAG_WAIT_TIMEOUT
+    first = min(G, 16 if d == 256 else 32)  # the heads that run together
+    assert torch.isnan(out[0, :first]).all()
+    good = torch.ones(out.shape[:2], dtype=torch.bool, device="cuda")
+    good[0, :first] = False
+    assert np.array_equal(bits(out[good]), bits(ref[good]))
+    assert np.array_equal(bits(w.attend(sel, cnt)), bits(ref))
+    assert pa.pa_get_error_flags(reset=True) == 0
