@@ -615,3 +615,15 @@ def test_wait_timeout_of_a_chosen_block(dtype, cache, B, G, d, K, stall_at):
     assert np.array_equal(bits(out[good]), bits(ref[good]))
     assert np.array_equal(bits(w.attend(sel, cnt)), bits(ref))
     assert pa.pa_get_error_flags(reset=True) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("B,H,G,Q", [(60, 8, 4, 1), (75, 6, 7, 1), (30, 8, 4, 2)])
+def test_many_rows_of_head_dim_128(dtype, B, H, G, Q):
+    """444 and more rows of up to 8 query heads: CTAs of three warps, four on an SM."""
+    assert B * Q * H >= 3 * 148
+    rng = np.random.default_rng(B)
+    w = Case([int(x) for x in rng.integers(Q, 500, B)], H, G, 128, dtype, Q=Q, seed=B + G)
+    sel, cnt = w.lists(13, 1)
+    w.check(w.attend(sel, cnt), w.model(sel, cnt), w.attend(sel, cnt, True))

@@ -395,3 +395,24 @@ def test_row_counts_past_the_limit_are_refused(kw):
     assert pa.lib.pa_select_blocks(*[f] * 7, ctypes.byref(p), None) == pa.PA_ERR_UNSUPPORTED
     assert pa.lib.pa_decode_selected(*[f] * 8, 0.1, ctypes.byref(p), None) == pa.PA_ERR_UNSUPPORTED
     assert pa.lib.pa_decode_sparse(*[f] * 10, 0.1, ctypes.byref(p), None) == pa.PA_ERR_UNSUPPORTED
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,B,H,Q,d,n,K", [("bfloat16", 112, 8, 1, 128, 256, 64), ("float16", 57, 8, 2, 128, 100, 40),
+                                               ("float32", 300, 3, 1, 64, 40, 9), ("float16", 223, 4, 1, 256, 130, 7),
+                                               ("bfloat16", 112, 8, 1, 64, 512, 200)])
+def test_choices_of_very_many_short_rows(dtype, B, H, Q, d, n, K):
+    """More than 888 rows of at most 512 blocks: CTAs of 128 threads."""
+    rng = np.random.default_rng(B + d)
+    G, N = 2, 300
+    assert B * Q * H > 6 * 148 and n <= 512
+    tables = rng.integers(0, N, (B, n)).astype(np.int32)   # blocks repeat: equal scores
+    codes, scales = M.boxes(rng.standard_normal((N, H, BS, d)).astype(np.float32))
+    lens = [int(x) for x in rng.integers(1, n * BS + 1, B)]
+    lens[3], lens[7] = n * BS, 0
+    q = to_store(rng.standard_normal((B, Q, H * G, d)), dtype)
+    pa.pa_get_error_flags(reset=True)
+    got = run_select(q, dtype, codes, scales, tables, lens, K, 1, 2, n * BS, Q)
+    assert pa.pa_get_error_flags(reset=True) == 0
+    want = M.choose(M.values(q), codes, scales, tables, lens, K, 1, 2, n * BS)
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
