@@ -150,9 +150,10 @@ __global__ void __launch_bounds__(kBoundsWarps * 32, D == 256 ? 4 : 6) block_bou
                     const int e = r * X::PER + p;
                     vl[c][e] = X::get(lo[c][r], p);
                     vh[c][e] = X::get(hi[c][r], p);
-                    if (sizeof(T) == 1) {  // codes: the keys are their products with the tile's scale
-                        vl[c][e] = __fmul_rn(vl[c][e], ks);
-                        vh[c][e] = __fmul_rn(vh[c][e], ks);
+                    if (sizeof(T) == 1) {  // codes: the keys are their products with the tile's scale (of either sign)
+                        const float x0 = __fmul_rn(vl[c][e], ks), x1 = __fmul_rn(vh[c][e], ks);
+                        vl[c][e] = min_nan(x0, x1);
+                        vh[c][e] = max_nan(x0, x1);
                     }
                     m = max_nan(m, max_nan(fabsf(vl[c][e]), fabsf(vh[c][e])));
                 }

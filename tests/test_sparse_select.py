@@ -416,3 +416,23 @@ def test_choices_of_very_many_short_rows(dtype, B, H, Q, d, n, K):
     assert pa.pa_get_error_flags(reset=True) == 0
     want = M.choose(M.values(q), codes, scales, tables, lens, K, 1, 2, n * BS)
     assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_boxes_of_odd_int8_scales(d):
+    """Scales that are negative, zero, infinite, NaN, very large and very small; code -128."""
+    rng = np.random.default_rng(d)
+    N = 9
+    kc = rng.integers(-127, 128, (N, 1, BS, d)).astype(np.int8)
+    kc[1, 0, 3, 5] = kc[0, 0, 1, 1] = -128
+    kc[2, 0, 0, 0] = 0
+    ks = np.array([-0.25, 0.5, np.inf, np.nan, 0, -3e36, 1e-44, -0.0, -1e-3], np.float32)[:, None]
+    with np.errstate(all="ignore"):
+        codes, s = M.boxes((kc.astype(np.float32) * ks[:, :, None, None]).astype(np.float32))
+    bounds = torch.zeros((N, 1, 2, d), dtype=torch.int8, device="cuda")
+    scales = torch.zeros((N, 1), device="cuda")
+    t = torch.arange(N, dtype=torch.int32, device="cuda")[None]
+    pa.pa_block_bounds(bounds, scales, to_dev(kc, "i"), t, torch.tensor([N * BS], dtype=torch.int32, device="cuda"), N * BS,
+                       k_scales=to_dev(ks, "f"))
+    assert np.array_equal(scales.cpu().numpy(), s) and np.array_equal(bounds.cpu().numpy(), codes)
