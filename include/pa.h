@@ -499,7 +499,9 @@ int pa_step_tables(int32_t *block_tables, const int32_t *seq_lens, const int32_t
  * by each.  The box of a partly filled block is not needed: a row's newest block is always
  * picked.  A full block whose keys are written anew (by pa_block_copy, say) needs its box again.
  * Covered are at most ceil(max_new_tokens / 16) blocks per sequence; a sequence that grew
- * by more sets PA_EFLAG_BAD_LENGTH.  Lengths above 16 * max_blocks_per_seq are cut to it.
+ * by more sets PA_EFLAG_BAD_LENGTH.  The launch has room for that many blocks of every sequence,
+ * whatever the lengths are, so max_new_tokens is best the most that one sequence gains between two
+ * calls (1 in a decode step), not the longest it may become.  Lengths above 16 * max_blocks_per_seq are cut to it.
  * Table entries outside the pool set PA_EFLAG_BAD_BLOCK and are skipped.
  * kv_dtype: PA_F32, PA_F16, PA_BF16 or PA_I8 (then k_scales); head_dim 64, 128 or 256.
  * key_cache and bounds are 16-byte aligned.
@@ -538,12 +540,14 @@ typedef struct pa_sparse_params {
  *   num_selected  [num_seqs * Q][num_kv_heads]     int32: min(n, K)
  * A row with n <= K takes all its blocks.  Otherwise the first sink_blocks, the last
  * recent_blocks and, of the others, those with the highest score, the lower index first
- * among equals.  The score estimates from above the largest product of a query head with
- * a key of the block; with q's codes of head g, in IEEE fp32,
+ * among equals.  The score is an estimate of the largest product of a query head with a key of
+ * the block, usually above it; with q's codes of head g, in IEEE fp32,
  *   s_g = max_j |q_j| / 127,  c_j = clamp(round_half_even(q_j / s_g), -127, 127)
  *   score = max_g (sum_j max(c_j * lo_j, c_j * hi_j)) * scale * s_g
  * over the query heads g of the KV head; the sum is of whole numbers, so the result does
- * not depend on any order of summation.  A head whose s_g is 0 or not finite has codes 0
+ * not depend on any order of summation.  The box holds the block's keys but for roundings of 2^-24
+ * of the largest; q's codes are rounded to the nearest, so a product q_g . k may exceed the score
+ * by up to s_g / 2 * sum_j |k_j| (and a few 2^-24 of itself).  A head whose s_g is 0 or not finite has codes 0
  * and s_g = 0.  A block whose scale is not finite scores +inf; one outside the pool scores
  * lowest (PA_EFLAG_BAD_BLOCK).  The boxes of the last recent_blocks are not used.
  * bounds 16-byte aligned.  Reads the fields of p that it names; k_scales, v_scales and

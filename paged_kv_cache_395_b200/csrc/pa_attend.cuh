@@ -14,12 +14,15 @@
 // on the M side for up to 8 heads and for int8 caches (stream_tokens_m), with the heads there for
 // 16 or 32 (stream_heads_m); either way a tile is read from shared memory once for all heads.
 // bf16 rounds P to 8 bits, too few for the result's own precision, so there P = hi + lo, two
-// products; fp16's 11 bits are enough.  An int8 tile's codes become exact fp16 / bf16 fragments in
+// products.  fp16's 11 bits move the result by at most 2^-11 of the largest |v|, as far as its own
+// rounding to fp16 may (as pa_decode does; in an fp32 output it is the largest error left).  An int8 tile's codes become exact fp16 / bf16 fragments in
 // registers; the block's K scale multiplies the scores, its V scale the block's product, in fp32.
 //
-// Bound by DRAM where there are rows enough (64 rows x 64 fp16 blocks of 16 x 128: 39.8 us, 5.9
+// Bound by DRAM where there are rows enough (512 rows x 64 fp16 blocks of 16 x 128: 45 us, 5.9
 // TB/s), by the chain list -> table entry -> tiles -> joining where there are few (8 rows: about
-// 5 us), and for int8 by instructions (128 rows x 128 blocks 19.1 us, 3.5 TB/s).
+// 5 us), and for int8 by each warp's chain tile -> unpacking -> MMA -> softmax -> unpacking -> MMA,
+// with three warps a scheduler and half of the issue slots used (128 rows x 128 blocks 19.6 us, 3.4
+// TB/s).  fp32: 512 rows x 64 blocks 142 us, 3.8 TB/s.
 #pragma once
 #include <cooperative_groups.h>
 

@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(128) attend_f32_kernel(const SparseArgs a) {
 }
 
 // CTAs per row: as many as the GPU holds at once, each warp with at least two blocks.  (128 rows of 128
-// int8 blocks in CTAs of four warps took 25.5 us with one CTA a row, 24.4 with two, 20.8 with three
-// and 28.2 with four, which no longer fit at once.)
+// int8 blocks in CTAs of four warps take 25.2 us with one CTA a row, 23.4 with two, 19.8 with three
+// and 26.8 with four, which no longer fit at once.)
 template <typename K>
 int cluster_of(ClusterRoom &room, K *kern, int64_t items, int blocks, int warps, size_t smem) {
     return room.largest(kern, items, blocks / (2 * warps), warps * 32, smem);
@@ -80,7 +80,7 @@ int launch_attend_t(SparseArgs a, cudaStream_t st) {
     if constexpr (NT == 1 && !C::I8 && D <= 128 && NW == 4)
         if ((int64_t)a.rows * a.H >= 3 * 148) return launch_attend_t<T, TKV, D, NT, 3>(a, st);
     // About a row per SM: one CTA with as many warps as the registers and shared memory hold, instead
-    // of a cluster of smaller ones that have to join their shares (128 int8 rows of 128 blocks 19.1 us
+    // of a cluster of smaller ones that have to join their shares (128 int8 rows of 128 blocks 19.6 us
     // against 19.8 with three CTAs of four warps; 128 rows of 32 heads 27.8 against 29.2 with their
     // choice).  Fewer rows with long lists: clusters of 8-warp CTAs, so that eight CTAs are 64 warps
     // (8 rows of 128 blocks 5.6 against 6.3 us, of 256 blocks 7.1 against 8.7, but of 64 blocks 5.3

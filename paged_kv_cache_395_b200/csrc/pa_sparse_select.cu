@@ -28,14 +28,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // ---------------------------------------------------------------------------
 // block_bounds: per (block, KV head) tile of 16 keys, per dim the smallest and largest
 // value, in eight bits with one scale; rounded outwards, so that the box still holds every
-// key.  A tile is read once (16 * D elements) and gives 2 D + 4 bytes: bound by the read.
+// key but for roundings of 2^-24 of the largest (the scale's own, which the clamp to 127 meets,
+// and the quotient's).  A tile is read once (16 * D elements) and gives 2 D + 4 bytes: bound by the read.
 // One warp per tile, tiles of one block's KV heads next to each other (they are one
 // contiguous piece of the cache); every lane keeps the columns of its 16-byte vectors in
 // registers, so the 16 rows need only one exchange at the end.  Instructions are the second
 // bound, so 16-bit caches are compared two values at a time, and a code's division is done by
 // the reciprocal unless the quotient is so near a whole number that only the division itself
 // tells on which side it lies.  The comparisons carry a NaN through to the scale.
-// 65536 fp16 tiles of 16 x 128: 53 us, 5.3 TB/s.
+// 65536 tiles of 16 x 128: fp16 49 us (5.8 TB/s), fp32 86 us (6.4 TB/s); int8 93 us (1.6 TB/s):
+// its 32 minima and maxima a lane as fp32 do not fit into the registers of six CTAs on an SM.
 // ---------------------------------------------------------------------------
 constexpr int kBoundsWarps = 8;  // per CTA
 
@@ -200,8 +202,8 @@ template <typename T>
 int bounds_d(const BoundsArgs &a, cudaStream_t st) {
     const int64_t items = (int64_t)a.B * a.W * a.H;
     // a tile per warp (the loop is for the largest grids): the CTAs' own turnover balances the SMs
-    // better than a grid of the resident ones that strides over the tiles (57.4 against 62 to 65 us
-    // for 65536 fp16 tiles of 16 x 128)
+    // better than a grid of the resident ones that strides over the tiles (49.1 against 55.0 us for
+    // 65536 fp16 tiles of 16 x 128)
     const int64_t ctas = (items + kBoundsWarps - 1) / kBoundsWarps;
     const dim3 grid((unsigned)(ctas < (1 << 22) ? ctas : (1 << 22)));
     cudaError_t e;

@@ -18,7 +18,9 @@
 // written by the same launch.  A step with prompts has so many that a cluster's few SMs
 // would be the bound, so a second kernel writes them over the whole GPU, from the tables and
 // lengths that the first one left (1024 sequences, 256 of them prompts, 526k slots: 102 us in one
-// cluster of 8 CTAs, 24.5 us this way; 64 sequences of one token: 7.0 us).
+// cluster of 8 CTAs, 24.5 us this way; 64 sequences of one token: 7.5 us).  The blocks given back in
+// a step with few tokens are one CTA's too: an ended request of 4096 tokens costs 0.1 us, one of
+// 131072 tokens 25 us (50 us with reference counts).
 #include <cooperative_groups.h>
 
 #include "pa_cluster.cuh"
